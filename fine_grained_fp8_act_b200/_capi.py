@@ -58,6 +58,13 @@ SIGNATURES = {
     "fg8_linear_static": (_INT, [_VP, _I64, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _I64, _VP, _SZ, _VP]),
     "fg8_dequantize_weight": (_INT, [_VP, _I64, _I64, _VP, _INT, _VP, _I64, _VP]),
     "fg8_scale_to_ue8m0": (_INT, [_VP, _I64, _VP, _VP, _VP]),
+    "fg8_rmsnorm_quant": (_INT, [_VP, _I64, _I64, _I64, _VP, _I64, _VP, ctypes.c_float, _VP, _VP, _INT, _INT, _VP,
+                                 _I64, _VP, _I64, _VP]),
+    "fg8_silu_mul_quant": (_INT, [_VP, _VP, _I64, _I64, _I64, _I64, _VP, _VP, _INT, _INT, _VP, _I64, _VP]),
+    "fg8_moe_route": (_INT, [_VP, _INT, _I64, _I64, _I64, _I64, _INT, ctypes.c_float, _VP, _VP, _VP]),
+    "fg8_moe_mlp_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64, _INT]),
+    "fg8_moe_mlp": (_INT, [_VP, _VP, _I64, _I64, _I64, _VP, _VP, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _I64,
+                           _INT, _VP, _SZ, _VP]),
     "fg8_check_device_status": (_INT, [_VP, _VP]),
     "fg8_set_wait_limit_ns": (None, [ctypes.c_uint64]),
     "fg8_set_test_stall": (None, [_INT]),
@@ -252,8 +259,36 @@ def fg8_scale_to_ue8m0(scale_f32, n, scale_e8m0, invalid_count, stream):
     _check("fg8_scale_to_ue8m0", lib().fg8_scale_to_ue8m0(scale_f32, n, scale_e8m0, invalid_count, stream))
 
 
+def fg8_rmsnorm_quant(x_bf16, M, K, ld_x, residual_bf16, ld_residual, weight_bf16, eps, xq_e4m3, x_scale, fmt, block,
+                      residual_out_bf16, ld_residual_out, y_bf16, ld_y, stream):
+    _check("fg8_rmsnorm_quant", lib().fg8_rmsnorm_quant(x_bf16, M, K, ld_x, residual_bf16, ld_residual, weight_bf16,
+                                                        eps, xq_e4m3, x_scale, fmt, block, residual_out_bf16,
+                                                        ld_residual_out, y_bf16, ld_y, stream))
+
+
+def fg8_silu_mul_quant(gate_bf16, up_bf16, M, K, ld_gate, ld_up, xq_e4m3, x_scale, fmt, block, y_bf16, ld_y, stream):
+    _check("fg8_silu_mul_quant", lib().fg8_silu_mul_quant(gate_bf16, up_bf16, M, K, ld_gate, ld_up, xq_e4m3, x_scale,
+                                                          fmt, block, y_bf16, ld_y, stream))
+
+
+def fg8_moe_route(logits, logits_bf16, T, E, ld_logits, k, renormalize, scale, ids, weights, stream):
+    _check("fg8_moe_route", lib().fg8_moe_route(logits, logits_bf16, T, E, ld_logits, k, renormalize, scale, ids,
+                                                weights, stream))
+
+
+def fg8_moe_mlp_workspace_bytes(T, k, E, H, I, fmt) -> int:
+    return int(lib().fg8_moe_mlp_workspace_bytes(T, k, E, H, I, fmt))
+
+
+def fg8_moe_mlp(x, x_scale, T, H, ld_x, ids, weights, k, E, I, w13_e4m3, w13_scale_inv, w2_e4m3, w2_scale_inv, y_bf16,
+                ld_y, fmt, workspace, workspace_bytes, stream):
+    _check("fg8_moe_mlp", lib().fg8_moe_mlp(x, x_scale, T, H, ld_x, ids, weights, k, E, I, w13_e4m3, w13_scale_inv,
+                                            w2_e4m3, w2_scale_inv, y_bf16, ld_y, fmt, workspace, workspace_bytes,
+                                            stream))
+
+
 def fg8_check_device_status(workspace, stream) -> int:
     """Returns the status code the previous calls on this workspace left: FG8_OK,
     FG8_ERR_TIMEOUT, or FG8_ERR_INVALID_ARG for an expert index >= E in a
-    grouped call; synchronizes the stream and clears the word; does not raise."""
+    grouped or few-token expert call; synchronizes the stream and clears the word; does not raise."""
     return int(lib().fg8_check_device_status(workspace, stream))

@@ -19,6 +19,7 @@ namespace {
 using namespace fg8;
 
 constexpr int64_t kMaxDim = 2147483647LL;
+constexpr int64_t kMaxNormWidth = 1LL << 30;  // row length of the fused norm and activation quantizers
 constexpr size_t kHeaderBytes = kWorkspaceHeaderBytes;  // status word, split-K counters
 constexpr size_t kAlign = 256;
 
@@ -1021,6 +1022,164 @@ fg8_status fg8_scale_to_ue8m0(const void* scale_f32, int64_t n, void* scale_e8m0
   if (fg8_status st = current_device(&dev); st != FG8_OK) return st;
   return cuda_status(launch_scale_to_e8m0(static_cast<const float*>(scale_f32), n, static_cast<uint8_t*>(scale_e8m0),
                                           invalid_count, dev.sms, static_cast<cudaStream_t>(stream)));
+}
+
+// ---- around the linears: norm, activation, routing, few-token experts ----
+// The fields both fused quantizers share; the checks of one bf16 operand.
+static bool rows_ok(const void* p, int64_t ld) { return ld % 8 == 0 && aligned16(p); }
+
+static NormActArgs norm_act_args(int64_t M, int64_t K, int block, void* xq_e4m3, void* x_scale) {
+  NormActArgs a{};
+  a.M = static_cast<int>(M);
+  a.K = static_cast<int>(K);
+  a.Kb = ceil_div(K, block);
+  a.group = block;
+  a.xq = static_cast<uint8_t*>(xq_e4m3);
+  a.xs = x_scale;
+  return a;
+}
+
+fg8_status fg8_rmsnorm_quant(const void* x_bf16, int64_t M, int64_t K, int64_t ld_x, const void* residual_bf16,
+                             int64_t ld_residual, const void* weight_bf16, float eps, void* xq_e4m3, void* x_scale,
+                             fg8_scale_fmt fmt, int block, void* residual_out_bf16, int64_t ld_residual_out,
+                             void* y_bf16, int64_t ld_y, void* stream) {
+  if (!fmt_ok(fmt) || (block != 128 && !small_block(block)) || M < 0 || K <= 0 || M > kMaxDim || K > kMaxNormWidth ||
+      ld_x < K || !(eps > 0.0f) || eps > 3.0e38f)
+    return FG8_ERR_INVALID_ARG;
+  if ((residual_bf16 != nullptr && ld_residual < K) || (residual_out_bf16 != nullptr && ld_residual_out < K) ||
+      (y_bf16 != nullptr && ld_y < K) || (residual_bf16 == nullptr) != (residual_out_bf16 == nullptr))
+    return FG8_ERR_INVALID_ARG;
+  if (M == 0) return FG8_OK;
+  if (x_bf16 == nullptr || weight_bf16 == nullptr || xq_e4m3 == nullptr || x_scale == nullptr)
+    return FG8_ERR_INVALID_ARG;
+  if (K % 16 != 0 || !rows_ok(x_bf16, ld_x) || !aligned16(weight_bf16) || !aligned16(xq_e4m3) ||
+      (fmt == FG8_SCALE_FLOAT && (reinterpret_cast<uintptr_t>(x_scale) & 3u) != 0) ||
+      (residual_bf16 != nullptr && (!rows_ok(residual_bf16, ld_residual) || !rows_ok(residual_out_bf16, ld_residual_out))) ||
+      (y_bf16 != nullptr && !rows_ok(y_bf16, ld_y)))
+    return FG8_ERR_ALIGNMENT;
+  DeviceInfo dev;
+  if (fg8_status st = current_device(&dev); st != FG8_OK) return st;
+  NormActArgs a = norm_act_args(M, K, block, xq_e4m3, x_scale);
+  a.x = x_bf16;
+  a.ld_x = ld_x;
+  a.x2 = residual_bf16;
+  a.ld_x2 = ld_residual;
+  a.weight = weight_bf16;
+  a.eps = eps;
+  a.x2_out = residual_out_bf16;
+  a.ld_x2_out = ld_residual_out;
+  a.y = y_bf16;
+  a.ld_y = ld_y;
+  return cuda_status(launch_rmsnorm_quant(a, fmt, static_cast<cudaStream_t>(stream)));
+}
+
+fg8_status fg8_silu_mul_quant(const void* gate_bf16, const void* up_bf16, int64_t M, int64_t K, int64_t ld_gate,
+                              int64_t ld_up, void* xq_e4m3, void* x_scale, fg8_scale_fmt fmt, int block,
+                              void* y_bf16, int64_t ld_y, void* stream) {
+  if (!fmt_ok(fmt) || (block != 128 && !small_block(block)) || M < 0 || K <= 0 || M > kMaxDim || K > kMaxNormWidth ||
+      ld_gate < K || ld_up < K || (y_bf16 != nullptr && ld_y < K))
+    return FG8_ERR_INVALID_ARG;
+  if (M == 0) return FG8_OK;
+  if (gate_bf16 == nullptr || up_bf16 == nullptr || xq_e4m3 == nullptr || x_scale == nullptr)
+    return FG8_ERR_INVALID_ARG;
+  if (K % 16 != 0 || !rows_ok(gate_bf16, ld_gate) || !rows_ok(up_bf16, ld_up) || !aligned16(xq_e4m3) ||
+      (fmt == FG8_SCALE_FLOAT && (reinterpret_cast<uintptr_t>(x_scale) & 3u) != 0) ||
+      (y_bf16 != nullptr && !rows_ok(y_bf16, ld_y)))
+    return FG8_ERR_ALIGNMENT;
+  DeviceInfo dev;
+  if (fg8_status st = current_device(&dev); st != FG8_OK) return st;
+  NormActArgs a = norm_act_args(M, K, block, xq_e4m3, x_scale);
+  a.x = gate_bf16;
+  a.ld_x = ld_gate;
+  a.x2 = up_bf16;
+  a.ld_x2 = ld_up;
+  a.y = y_bf16;
+  a.ld_y = ld_y;
+  return cuda_status(launch_silu_mul_quant(a, fmt, dev.sms, static_cast<cudaStream_t>(stream)));
+}
+
+fg8_status fg8_moe_route(const void* logits, int logits_bf16, int64_t T, int64_t E, int64_t ld_logits, int64_t k,
+                         int renormalize, float scale, int32_t* ids, float* weights, void* stream) {
+  if (T < 0 || T > kMaxDim || E <= 0 || E > kRouteMaxExperts || k <= 0 || k > kRouteMaxTopk || k > E ||
+      ld_logits < E || !(scale - scale == 0.0f))
+    return FG8_ERR_INVALID_ARG;
+  if (T == 0) return FG8_OK;
+  if (logits == nullptr || ids == nullptr || weights == nullptr) return FG8_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(logits) & (logits_bf16 ? 1u : 3u)) != 0 ||
+      (reinterpret_cast<uintptr_t>(ids) & 3u) != 0 || (reinterpret_cast<uintptr_t>(weights) & 3u) != 0)
+    return FG8_ERR_ALIGNMENT;
+  DeviceInfo dev;
+  if (fg8_status st = current_device(&dev); st != FG8_OK) return st;
+  RouteArgs a{};
+  a.logits = logits;
+  a.ld = ld_logits;
+  a.bf16 = logits_bf16 != 0;
+  a.T = static_cast<int>(T);
+  a.E = static_cast<int>(E);
+  a.k = static_cast<int>(k);
+  a.renormalize = renormalize != 0;
+  a.scale = scale;
+  a.ids = ids;
+  a.weights = weights;
+  return cuda_status(launch_moe_route(a, static_cast<cudaStream_t>(stream)));
+}
+
+static fg8_status check_moe_shape(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, int fmt) {
+  if (!fmt_ok(fmt) || T < 0 || T > kMoeMaxTokens || k <= 0 || k > kMoeMaxTopk || T * k > kMoeMaxPairs || E <= 0 ||
+      E > kMoeMaxExperts || H <= 0 || H > kMoeMaxHidden || I <= 0 || I > kMaxDim / 4)
+    return FG8_ERR_INVALID_ARG;
+  if (E * 2 * I + 256 > kMaxDim || E * H + 256 > kMaxDim) return FG8_ERR_INVALID_ARG;
+  if (H % 16 != 0 || I % 16 != 0) return FG8_ERR_ALIGNMENT;
+  return FG8_OK;
+}
+
+size_t fg8_moe_mlp_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, fg8_scale_fmt fmt) {
+  if (check_moe_shape(T, k, E, H, I, fmt) != FG8_OK) return 0;
+  return moe_workspace_need(static_cast<int>(T), static_cast<int>(k), static_cast<int>(E), static_cast<int>(H),
+                            static_cast<int>(I), fmt);
+}
+
+fg8_status fg8_moe_mlp(const void* x, const void* x_scale, int64_t T, int64_t H, int64_t ld_x, const int32_t* ids,
+                       const float* weights, int64_t k, int64_t E, int64_t I, const void* w13_e4m3,
+                       const void* w13_scale_inv, const void* w2_e4m3, const void* w2_scale_inv, void* y_bf16,
+                       int64_t ld_y, fg8_scale_fmt fmt, void* workspace, size_t workspace_bytes, void* stream) {
+  if (fg8_status st = check_moe_shape(T, k, E, H, I, fmt); st != FG8_OK) return st;
+  if (ld_x < H || ld_y < H || (x_scale != nullptr && ld_x != H)) return FG8_ERR_INVALID_ARG;
+  if (T == 0) return FG8_OK;
+  if (x == nullptr || ids == nullptr || weights == nullptr || w13_e4m3 == nullptr || w13_scale_inv == nullptr ||
+      w2_e4m3 == nullptr || w2_scale_inv == nullptr || y_bf16 == nullptr)
+    return FG8_ERR_INVALID_ARG;
+  if (!aligned16(x) || (x_scale == nullptr && ld_x % 8 != 0) || !rows_ok(y_bf16, ld_y) || !aligned16(w13_e4m3) ||
+      !aligned16(w2_e4m3) || !aligned16(w13_scale_inv) || !aligned16(w2_scale_inv) ||
+      (reinterpret_cast<uintptr_t>(x_scale) & (fmt == FG8_SCALE_FLOAT ? 3u : 0u)) != 0 ||
+      (reinterpret_cast<uintptr_t>(ids) & 3u) != 0 || (reinterpret_cast<uintptr_t>(weights) & 3u) != 0)
+    return FG8_ERR_ALIGNMENT;
+  if (fg8_status st = check_workspace(workspace, workspace_bytes, fg8_moe_mlp_workspace_bytes(T, k, E, H, I, fmt));
+      st != FG8_OK)
+    return st;
+  DeviceInfo dev;
+  if (fg8_status st = current_device(&dev); st != FG8_OK) return st;
+  MoeArgs a{};
+  a.x = x;
+  a.ld_x = ld_x;
+  a.x_scale = x_scale;
+  a.T = static_cast<int>(T);
+  a.k = static_cast<int>(k);
+  a.E = static_cast<int>(E);
+  a.H = static_cast<int>(H);
+  a.I = static_cast<int>(I);
+  a.ids = ids;
+  a.weights = weights;
+  a.w13 = static_cast<const uint8_t*>(w13_e4m3);
+  a.s13 = w13_scale_inv;
+  a.w2 = static_cast<const uint8_t*>(w2_e4m3);
+  a.s2 = w2_scale_inv;
+  a.y = y_bf16;
+  a.ld_y = ld_y;
+  a.ws = static_cast<uint8_t*>(workspace);
+  a.wait_limit_ns = g_wait_limit_ns.load();
+  a.test_stall = g_test_stall.load();
+  return cuda_status(launch_moe_mlp(a, fmt, dev.sms, static_cast<cudaStream_t>(stream)));
 }
 
 fg8_status fg8_check_device_status(void* workspace, void* stream) {

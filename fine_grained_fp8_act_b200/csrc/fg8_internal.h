@@ -47,6 +47,68 @@ struct ActQuantArgs {
 
 cudaError_t launch_act_quant(const ActQuantArgs& a, int fmt, int num_sms, cudaStream_t s);
 
+// RMS norm or silu(gate) * up, quantized as an activation (norm_act.cu):
+// codes [M, K] (row stride K) and row-major scales [M, ceil(K / group)].
+struct NormActArgs {
+  const void* x;       // bf16 [M, K], row stride ld_x: x, or the gate
+  int64_t ld_x;
+  const void* x2;      // bf16 [M, K], row stride ld_x2: the residual (nullptr: none), or up
+  int64_t ld_x2;
+  const void* weight;  // rms norm: bf16 [K]
+  float eps;
+  int M, K, Kb;
+  int group;           // 128, 64 or 32
+  uint8_t* xq;
+  void* xs;
+  void* x2_out;        // rms norm: bf16(x + residual), row stride ld_x2_out, or nullptr
+  int64_t ld_x2_out;
+  void* y;             // bf16 of the values that were quantized, row stride ld_y, or nullptr
+  int64_t ld_y;
+};
+cudaError_t launch_rmsnorm_quant(const NormActArgs& a, int fmt, cudaStream_t s);
+cudaError_t launch_silu_mul_quant(const NormActArgs& a, int fmt, int num_sms, cudaStream_t s);
+
+// Softmax routing of T tokens over E experts (moe_route.cu).
+struct RouteArgs {
+  const void* logits;  // float32 or bf16 [T, E], row stride ld
+  int64_t ld;
+  int bf16;
+  int T, E, k;
+  int renormalize;
+  float scale;
+  int32_t* ids;        // [T, k]
+  float* weights;      // [T, k]
+};
+constexpr int kRouteMaxExperts = 1024;
+constexpr int kRouteMaxTopk = 32;
+cudaError_t launch_moe_route(const RouteArgs& a, cudaStream_t s);
+
+// The mixture-of-experts layer for few tokens (moe.cu).
+constexpr int kMoeMaxTokens = 256;
+constexpr int kMoeMaxTopk = 32;
+constexpr int kMoeMaxPairs = 4096;   // tokens x experts per token
+constexpr int kMoeMaxExperts = 1024;
+constexpr int kMoeMaxHidden = 16384;
+struct MoeArgs {
+  const void* x;       // bf16 [T, H], row stride ld_x; or, with x_scale, e4m3 [T, H]
+  int64_t ld_x;
+  const void* x_scale; // nullptr, or [T, ceil(H/128)] float32 / UE8M0
+  int T, k, E, H, I;
+  const int32_t* ids;  // [T, k]
+  const float* weights;
+  const uint8_t* w13;  // e4m3 [E, 2I, H]
+  const void* s13;
+  const uint8_t* w2;   // e4m3 [E, H, I]
+  const void* s2;
+  void* y;             // bf16 [T, H], row stride ld_y
+  int64_t ld_y;
+  uint8_t* ws;         // workspace (moe_ws_layout)
+  uint64_t wait_limit_ns;
+  int test_stall;
+};
+size_t moe_workspace_need(int T, int k, int E, int H, int I, int fmt);
+cudaError_t launch_moe_mlp(const MoeArgs& a, int fmt, int num_sms, cudaStream_t s);
+
 cudaError_t launch_weight_quant(const void* w, int64_t ld_w, int N, int K, uint8_t* wq, void* ws, int fmt,
                                 cudaStream_t s);
 // block x block weight blocks, block 32 or 64 (weight_block_size = (block,

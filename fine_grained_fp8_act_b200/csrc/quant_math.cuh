@@ -71,6 +71,9 @@ __device__ __forceinline__ void unpack_bf16x8(const uint4& v, float (&f)[8]) {
   }
 }
 
+// g / (1 + exp(-g)) * u in float32.
+__device__ __forceinline__ float silu_mul(float g, float u) { return __fdiv_rn(g, 1.0f + expf(-g)) * u; }
+
 // Quantize 16 values (two 16-byte bf16 loads) with the group's scale;
 // returns 16 packed e4m3 bytes.
 template <int FMT>

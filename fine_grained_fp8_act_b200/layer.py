@@ -328,6 +328,137 @@ def scale_to_ue8m0(scale: torch.Tensor) -> Tuple[torch.Tensor, int]:
     return out.view(torch.float8_e8m0fnu), int(bad.item())
 
 
+def _quantized_outputs(M: int, K: int, fmt: int, block: int, device):
+    if block not in (128, 64, 32):
+        raise ValueError(f"block must be 128, 64 or 32, got {block!r}")
+    return (torch.empty((M, K), dtype=torch.float8_e4m3fn, device=device),
+            torch.empty((M, _cdiv(K, block)), dtype=_SCALE_DTYPES[fmt], device=device))
+
+
+def _check_like(t, name: str, x: torch.Tensor):
+    """t: bf16 rows of x's shape, on its device."""
+    _check_bf16_matrix(t, name)
+    if t.shape != x.shape or t.device != x.device:
+        raise ValueError(f"{name} must be {tuple(x.shape)} on {x.device}")
+
+
+def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
+                  scale_fmt="float", block: int = 128, return_y: bool = False,
+                  residual_out: Optional[torch.Tensor] = None):
+    """RMS norm fused with the activation quantization: z = x + residual (or x),
+    v = z / sqrt(mean(z^2) + eps) * weight, all float32, then quantize_act's codes
+    and scales of v.  x and residual bf16 [M, K], weight bf16 [K].  Returns
+    (xq, x_scale, bf16(z) or None without a residual, bf16(v) if return_y else
+    None): xq and x_scale are what gemm_prequant and moe_mlp take.  residual_out
+    (default: a new tensor) may be `residual` itself, to update it in place."""
+    fmt = scale_fmt_code(scale_fmt)
+    _check_bf16_matrix(x, "x")
+    M, K = x.shape
+    _check_tensor(weight, "weight", (K,), (torch.bfloat16,), x.device)
+    if residual is not None:
+        _check_like(residual, "residual", x)
+    if residual_out is not None:
+        if residual is None:
+            raise ValueError("residual_out needs a residual")
+        _check_like(residual_out, "residual_out", x)
+    _check_cuda(x, "x")
+    xq, xs = _quantized_outputs(M, K, fmt, block, x.device)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
+    y = torch.empty((M, K), dtype=torch.bfloat16, device=x.device) if return_y else None
+    with torch.cuda.device(x.device):
+        C.fg8_rmsnorm_quant(x.data_ptr(), M, K, x.stride(0), 0 if residual is None else residual.data_ptr(),
+                            K if residual is None else residual.stride(0), weight.data_ptr(), eps, xq.data_ptr(),
+                            xs.data_ptr(), fmt, block, 0 if residual_out is None else residual_out.data_ptr(),
+                            K if residual_out is None else residual_out.stride(0), 0 if y is None else y.data_ptr(),
+                            K, _stream(x))
+    return xq, xs, residual_out, y
+
+
+def silu_mul_quant(gate: torch.Tensor, up: torch.Tensor, scale_fmt="float", block: int = 128,
+                   return_y: bool = False):
+    """v = silu(gate) * up in float32, then quantize_act's codes and scales of v:
+    gate and up bf16 [M, K] (for instance y[:, :K] and y[:, K:] of one gate/up
+    projection).  Returns (xq, x_scale, bf16(v) if return_y else None)."""
+    fmt = scale_fmt_code(scale_fmt)
+    _check_bf16_matrix(gate, "gate")
+    _check_like(up, "up", gate)
+    _check_cuda(gate, "gate")
+    M, K = gate.shape
+    xq, xs = _quantized_outputs(M, K, fmt, block, gate.device)
+    y = torch.empty((M, K), dtype=torch.bfloat16, device=gate.device) if return_y else None
+    with torch.cuda.device(gate.device):
+        C.fg8_silu_mul_quant(gate.data_ptr(), up.data_ptr(), M, K, gate.stride(0), up.stride(0), xq.data_ptr(),
+                             xs.data_ptr(), fmt, block, 0 if y is None else y.data_ptr(), K, _stream(gate))
+    return xq, xs, y
+
+
+def moe_route(logits: torch.Tensor, k: int, renormalize: bool = True,
+              scale: float = 1.0) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Expert routing: logits [T, E] float32 or bf16 -> (ids int32 [T, k], weights
+    float32 [T, k]), the k largest logits of each token in falling order (ties: the
+    lowest index) and their softmax weights, normalized over the k chosen (or all
+    E) experts, times scale.  Logits of -inf or NaN are never chosen: id -1,
+    weight 0 where fewer than k are left."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or logits.dtype not in (torch.float32,
+                                                                                         torch.bfloat16):
+        raise ValueError("logits must be a 2-D float32 or bf16 tensor")
+    if logits.stride(1) != 1 or (logits.shape[0] > 1 and logits.stride(0) < logits.shape[1]):
+        raise ValueError("logits must have unit stride in its last dimension and rows that do not overlap")
+    T, E = logits.shape
+    if not 1 <= k <= min(E, 32):
+        raise ValueError(f"k must be between 1 and min({E}, 32), got {k}")
+    _check_cuda(logits, "logits")
+    ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    with torch.cuda.device(logits.device):
+        C.fg8_moe_route(logits.data_ptr(), 1 if logits.dtype == torch.bfloat16 else 0, T, E, logits.stride(0), k,
+                        1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), _stream(logits))
+    return ids, weights
+
+
+def moe_mlp(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: torch.Tensor, w13_scale_inv: torch.Tensor,
+            w2: torch.Tensor, w2_scale_inv: torch.Tensor, scale_fmt="ue8m0", x_scale: Optional[torch.Tensor] = None,
+            out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A whole mixture-of-experts layer for few tokens (T <= 256): y [T, H] bf16 =
+    sum over j of weights[t, j] * W2[e] . (silu(gate) * up), e = ids[t, j], gate and
+    up the halves of W13[e] . x[t].  x bf16 [T, H], or e4m3 codes with x_scale (as
+    rmsnorm_quant or quantize_act return them); ids int32 [T, k] (negative: the slot
+    is skipped) and weights float32 [T, k] as moe_route returns them; w13 e4m3
+    [E, 2I, H] (gate rows, then up rows), w2 e4m3 [E, H, I], with their 128 x 128
+    block scales.  For many tokens use grouped_linear."""
+    fmt = scale_fmt_code(scale_fmt)
+    if x_scale is None:
+        _check_bf16_matrix(x, "x")
+    elif not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    if not isinstance(w13, torch.Tensor) or not isinstance(w2, torch.Tensor) or w13.dim() != 3 or w2.dim() != 3:
+        raise ValueError("w13 must be [E, 2I, H] and w2 [E, H, I]")
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be [T, k]")
+    (T, H), k = x.shape, int(ids.shape[1])
+    E, I = int(w13.shape[0]), int(w2.shape[2])
+    if x_scale is not None:
+        _check_tensor(x, "x", (T, H), _E4M3, x.device)
+        _check_tensor(x_scale, "x_scale", (T, _cdiv(H, 128)), _scale_dtypes(fmt), x.device)
+    _check_tensor(ids, "ids", (T, k), (torch.int32,), x.device)
+    _check_tensor(weights, "weights", (T, k), (torch.float32,), x.device)
+    _check_tensor(w13, "w13", (E, 2 * I, H), _E4M3, x.device)
+    _check_tensor(w13_scale_inv, "w13_scale_inv", (E, _cdiv(2 * I, 128), _cdiv(H, 128)), _scale_dtypes(fmt), x.device)
+    _check_tensor(w2, "w2", (E, H, I), _E4M3, x.device)
+    _check_tensor(w2_scale_inv, "w2_scale_inv", (E, _cdiv(H, 128), _cdiv(I, 128)), _scale_dtypes(fmt), x.device)
+    y = _output(out, T, H, x.device)
+    _check_cuda(x, "x")
+    nbytes = C.fg8_moe_mlp_workspace_bytes(T, k, E, H, I, fmt)  # 0: the call below reports why
+    ws = _workspace(nbytes, x.device, workspace)
+    with torch.cuda.device(x.device):
+        C.fg8_moe_mlp(x.data_ptr(), 0 if x_scale is None else x_scale.data_ptr(), T, H, x.stride(0), ids.data_ptr(),
+                      weights.data_ptr(), k, E, I, w13.data_ptr(), w13_scale_inv.data_ptr(), w2.data_ptr(),
+                      w2_scale_inv.data_ptr(), y.data_ptr(), y.stride(0), fmt, ws.data_ptr(),
+                      ws.numel() * ws.element_size(), _stream(x))
+    return y
+
+
 class FP8Linear(torch.nn.Module):
     """Inference linear layer holding a quantized weight ([zh] §一 FP8Linear):
     weight float8_e4m3fn [out, in], weight_scale_inv per block x block block

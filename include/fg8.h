@@ -377,11 +377,95 @@ FG8_API fg8_status fg8_dequantize_weight(const void* wq_e4m3, int64_t N, int64_t
 FG8_API fg8_status fg8_scale_to_ue8m0(const void* scale_f32, int64_t n, void* scale_e8m0, uint32_t* invalid_count,
                                       void* stream);
 
+/* RMS norm of x (with a residual added first), quantized as an activation in
+ * one pass: the layer in front of a block's first FP8 linear.
+ *   z = x + residual;  v = z * (1 / sqrt(mean(z^2) + eps)) * weight
+ * in float32, then scales and codes of v exactly as fg8_quantize_act_block
+ * makes them of its input (v itself is not rounded to bf16 first).
+ *   x_bf16        [M, K] bf16, row stride ld_x
+ *   residual_bf16 [M, K] bf16, row stride ld_residual, or NULL (z = x)
+ *   weight_bf16   [K] bf16
+ *   eps           > 0 and finite
+ *   xq_e4m3       [M, K] e4m3fn, row stride K (output)
+ *   x_scale       [M, ceil(K/block)] row-major float32 or UE8M0 (output)
+ *   residual_out_bf16 [M, K] bf16(z), row stride ld_residual_out (output; NULL
+ *                 exactly when residual_bf16 is).  It may be the residual's
+ *                 or x's own buffer with the same row stride; otherwise no
+ *                 output overlaps an input or another output.
+ *   y_bf16        [M, K] bf16(v), row stride ld_y, or NULL (output: what a
+ *                 router or an unquantized layer reads)
+ *   block         128, 64 or 32; K <= 2^30
+ * Checks as fg8_quantize_act for every bf16 operand (pointers 16-byte
+ * aligned, row strides % 8); M == 0 is a no-op. */
+FG8_API fg8_status fg8_rmsnorm_quant(const void* x_bf16, int64_t M, int64_t K, int64_t ld_x,
+                                     const void* residual_bf16, int64_t ld_residual, const void* weight_bf16,
+                                     float eps, void* xq_e4m3, void* x_scale, fg8_scale_fmt fmt, int block,
+                                     void* residual_out_bf16, int64_t ld_residual_out, void* y_bf16, int64_t ld_y,
+                                     void* stream);
+
+/* silu(gate) * up, quantized as an activation in one pass: what stands
+ * between a gate/up projection and the down projection.
+ *   v = gate / (1 + exp(-gate)) * up
+ * in float32, then scales and codes of v as fg8_quantize_act_block's.
+ *   gate_bf16, up_bf16 [M, K] bf16, row strides ld_gate, ld_up (the two
+ *                 halves of one [M, 2K] output have ld = 2K and up = gate + K)
+ *   xq_e4m3, x_scale, block, y_bf16 as fg8_rmsnorm_quant.  No output overlaps
+ *                 an input.  Checks as there. */
+FG8_API fg8_status fg8_silu_mul_quant(const void* gate_bf16, const void* up_bf16, int64_t M, int64_t K,
+                                      int64_t ld_gate, int64_t ld_up, void* xq_e4m3, void* x_scale,
+                                      fg8_scale_fmt fmt, int block, void* y_bf16, int64_t ld_y, void* stream);
+
+/* Expert routing: for each token the k largest of its E logits in falling
+ * order (equal logits: the lowest index first) and their softmax weights,
+ *   weights[t, j] = scale * exp(l_j - l_max) / sum,
+ * the sum over the k chosen logits (renormalize != 0) or over all E.
+ *   logits   [T, E] float32, or bf16 with logits_bf16 != 0; row stride ld_logits
+ *   ids      [T, k] int32 (output), weights [T, k] float32 (output)
+ * A logit of -inf or NaN is never chosen: a token with fewer than k others
+ * gets id -1 and weight 0 in the slots left over.  1 <= k <= min(E, 32),
+ * E <= 1024, scale finite; pointers aligned to their element. */
+FG8_API fg8_status fg8_moe_route(const void* logits, int logits_bf16, int64_t T, int64_t E, int64_t ld_logits,
+                                 int64_t k, int renormalize, float scale, int32_t* ids, float* weights,
+                                 void* stream);
+
+/* A whole mixture-of-experts layer for few tokens (decoding), on unsorted,
+ * unpadded tokens; fg8_grouped_linear is the form for many.
+ *   y[t] = sum over j of weights[t, j] * W2[e] . h[t, j],  e = ids[t, j]
+ *   h[t, j] = silu(W13[e][:I] . x[t]) * (W13[e][I:] . x[t])
+ * x and h are quantized per token in 1 x 128 groups as fg8_linear quantizes
+ * its input (h from float32, without a bf16 step in between); products are
+ * accumulated in float32 with float32 or UE8M0 scales as in fg8_linear; the
+ * sum over j runs in the order of j in float32; y is rounded once.
+ *   x        bf16 [T, H], row stride ld_x (x_scale NULL); or e4m3 [T, H] with
+ *            x_scale [T, ceil(H/128)] float32 / UE8M0 as fg8_quantize_act or
+ *            fg8_rmsnorm_quant write them (ld_x == H)
+ *   ids      [T, k] int32: a negative id's slot is skipped (an expert of
+ *            another rank, padding); an id >= E is skipped too and leaves
+ *            FG8_ERR_INVALID_ARG in the status word.  The same expert may
+ *            stand in several slots of a token: each counts.
+ *   weights  [T, k] float32
+ *   w13_e4m3 [E, 2I, H] e4m3fn: the I gate rows, then the I up rows;
+ *            w13_scale_inv [E, ceil(2I/128), ceil(H/128)]
+ *   w2_e4m3  [E, H, I] e4m3fn; w2_scale_inv [E, ceil(H/128), ceil(I/128)]
+ *   y_bf16   [T, H], row stride ld_y (output; a token without a valid slot
+ *            gets zeros)
+ *   workspace >= fg8_moe_mlp_workspace_bytes, with the header rules of
+ *            fg8_linear
+ * T <= 256, k <= 32, T * k <= 4096, E <= 1024, H <= 16384, H % 16 == 0,
+ * I % 16 == 0, E * 2I + 256 and E * H + 256 <= 2^31 - 1.  T == 0 is a no-op. */
+FG8_API size_t fg8_moe_mlp_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, fg8_scale_fmt fmt);
+FG8_API fg8_status fg8_moe_mlp(const void* x, const void* x_scale, int64_t T, int64_t H, int64_t ld_x,
+                               const int32_t* ids, const float* weights, int64_t k, int64_t E, int64_t I,
+                               const void* w13_e4m3, const void* w13_scale_inv, const void* w2_e4m3,
+                               const void* w2_scale_inv, void* y_bf16, int64_t ld_y, fg8_scale_fmt fmt,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronizes `stream`, reads and clears the status word a previous
- * fg8_linear / fg8_gemm_prequant / fg8_grouped_linear left in `workspace`:
+ * fg8_linear / fg8_gemm_prequant / fg8_grouped_linear / fg8_moe_mlp left in `workspace`:
  * FG8_OK; FG8_ERR_TIMEOUT if one of its device-side waits gave up (the
  * kernel then returned early; y is unspecified); FG8_ERR_INVALID_ARG if
- * fg8_grouped_linear met an expert index >= E (those blocks were skipped). */
+ * fg8_grouped_linear or fg8_moe_mlp met an expert index >= E (those blocks
+ * or slots were skipped). */
 FG8_API fg8_status fg8_check_device_status(void* workspace, void* stream);
 
 /* Upper bound, in nanoseconds, on any single device-side wait of the GEMM
