@@ -8,12 +8,45 @@
 // that quantization and until y's one rounding to bf16.
 //
 // With few tokens the layer is bound by reading the reached experts' e4m3
-// weights once (3 H I bytes an expert).
+// weights once (3 H I bytes an expert), so both kernels are weight streams:
+// moe_kernel<UP> computes h (codes and scales, to the workspace),
+// moe_kernel<DOWN> the down products and y.  Both run one CTA per SM.
 //
-// First form: one warp per weight row and routed pair, plain loads.
+// Work: the routed pairs (token, slot) are grouped by expert in chunks of at
+// most 32; chunk and 256-row weight tile (128 gate and the matching 128 up
+// rows, or 256 rows of W2) make a unit of Kb K-blocks of 128.  The units of
+// all chunks in a row (one expert's tiles, its chunks innermost, so that a
+// second chunk finds the tile in L2) are cut into equal runs of K-blocks, one
+// per CTA: every SM streams the same number of bytes whatever the routing is.
+// A unit that a cut divides is added up in CTA order by whichever of its CTAs
+// finishes last, so the result does not depend on which one that is.
+//
+// Roles (320 threads):
+//   warp 0      producer: per K-block, two TMA boxes of 128 x 128 weights
+//   warp 1      MMA issuer: weights are the tensor core's M side (2 x 128
+//               rows), the chunk's tokens its N side (16 or 32 columns)
+//   warps 2-5   activations: each K-block's token rows gathered by pair into
+//               the MMA's B operand (128-byte swizzle), quantized on the way
+//               if x is bf16; their scales and the tile's weight scales into
+//               a ring.  Loads are issued before the ring slot is free.
+//   warps 6-9   epilogue: thread = weight row.  Each K-block's partial
+//               products land in a TMEM buffer of their own and are promoted,
+//               acc += P * (sx * sw), then finished per unit: silu(gate) * up,
+//               the 128-row group's amax, scale and codes (UP); the pair's
+//               products, and by the last unit of a row tile the weighted
+//               sums over the slots (DOWN).
+//
+// DOWN is launched to overlap UP's end: its first weight tiles are on their
+// way while UP's last units finish; only the warps that read h wait for it.
+//
+// Every wait is bounded; on expiry the kernel records FG8_ERR_TIMEOUT in the
+// status word, drains its copies and tensor-core ops, frees TMEM and returns.
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
+
+#include <atomic>
 
 #include "fg8_internal.h"
 #include "ptx.cuh"
@@ -24,126 +57,739 @@ namespace {
 
 using namespace qm;
 
+constexpr uint32_t kTimeoutStatus = 6u;     // FG8_ERR_TIMEOUT
+constexpr uint32_t kInvalidArgStatus = 1u;  // FG8_ERR_INVALID_ARG
+constexpr uint64_t kDrainNs = 1000000000ull;
+
+constexpr int kMaxGrid = 160;   // split-unit counters and partials are sized for this many CTAs
+constexpr int kRowTile = 256;   // weight rows of a unit: two MMAs of 128
+constexpr int kChunk = 32;      // tokens of a unit
+constexpr int kMinRun = 2;      // K-blocks per CTA below which fewer CTAs share the work
+constexpr int kMaxJobs = kMoeMaxExperts + kMoeMaxPairs / kChunk;
+constexpr size_t kPartFloats = static_cast<size_t>(kRowTile) * kChunk;
+static_assert(kMaxGrid + kMoeMaxHidden / kRowTile <= kHeaderCounters, "counters in the workspace header");
+
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
+// [header | h codes [P, I] | h scales float32 [P, ceil(I/128)] | partial
+// sums of split units, two per CTA | down products float32 [P, H]]
 struct MoeWs {
-  size_t xq, xs, hq, hs, part, total;
+  size_t hq, hs, split, part, total;
 };
 
 MoeWs moe_ws_layout(int64_t T, int64_t k, int64_t H, int64_t I) {
   MoeWs w;
-  const int64_t P = T * k, Hb = (H + 127) / 128, Ib = (I + 127) / 128;
-  w.xq = kWorkspaceHeaderBytes;
-  w.xs = align256(w.xq + T * H);
-  w.hq = align256(w.xs + T * Hb * 4);
+  const int64_t P = T * k, Ib = (I + 127) / 128;
+  w.hq = kWorkspaceHeaderBytes;
   w.hs = align256(w.hq + P * I);
-  w.part = align256(w.hs + P * Ib * 4);
+  w.split = align256(w.hs + P * Ib * 4);
+  w.part = align256(w.split + 2 * kMaxGrid * kPartFloats * 4);
   w.total = align256(w.part + P * H * 4);
   return w;
 }
 
+struct MoeParams {
+  const void* x;        // UP: bf16 [T, H] (row stride ld_x) or e4m3 codes [T, H]
+  int64_t ld_x;
+  const void* x_scale;  // UP on codes: [T, Hb]
+  const int32_t* ids;
+  const float* weights;
+  const void* w_scale;  // this kernel's weight scales [E][Nb][Kb]
+  int T, k, E, H, I;
+  int K, Kb, Nb;        // products' length and its blocks; scale rows per expert
+  int tiles;            // row tiles per expert
+  uint8_t* hq;
+  float* hs;
+  float* split;
+  float* part;
+  void* y;
+  int64_t ld_y;
+  uint32_t* status;
+  uint32_t* counters;
+  uint64_t wait_limit_ns;
+  int test_stall;
+};
+
+enum Phase : int { UP = 0, DOWN = 1 };
+
+template <int PHASE_, int FMT_, bool CODES_>
+struct MoeCfg {
+  static constexpr int PHASE = PHASE_, FMT = FMT_;
+  static constexpr bool CODES = CODES_;  // the activations come as codes and scales
+  static constexpr int kW = 2 * 128 * 128, kX = kChunk * 128, kStage = kW + kX;
+  static constexpr int STAGES = 5;
+  static constexpr int kSlots = 8;                       // scale ring
+  static constexpr int kSlotFloats = kChunk + 8;
+  static constexpr int kNumAcc = 4, kAccCols = 2 * kChunk;
+  static constexpr int kFillWarp0 = 2, kFillWarps = 4, kEpiWarp0 = 6, kEpiThreads = 128;
+  static constexpr int kThreads = kEpiWarp0 * 32 + kEpiThreads;
+  static constexpr int kOffSc = STAGES * kStage;
+  static constexpr int kOffStage = kOffSc + kSlots * kSlotFloats * 4;  // [kChunk][128] float32
+  static constexpr int kOffList = kOffStage + kChunk * 128 * 4;        // pairs by expert
+  static constexpr int kOffCnt = kOffList + kMoeMaxPairs * 2;          // pairs per expert
+  static constexpr int kOffOff = kOffCnt + kMoeMaxExperts * 2;         // first pair
+  static constexpr int kOffJob = kOffOff + kMoeMaxExperts * 2;         // first chunk
+  static constexpr int kOffJobE = kOffJob + kMoeMaxExperts * 2;        // expert of each chunk
+  static constexpr int kOffBar = (kOffJobE + kMaxJobs * 2 + 15) / 16 * 16;
+  static constexpr int kSmem = 1024 + kOffBar + 512;
+  static_assert(kSmem <= 232448, "shared memory budget");
+  static_assert(kStage % 1024 == 0, "swizzled operands start on 1024-byte boundaries");
+  static_assert((3 * STAGES + 2 * kNumAcc + 2 * kSlots + 2) * 8 + 32 <= 512, "barrier area");
+  static_assert(kSlots % kFillWarps == 0, "a scale slot always belongs to the same warp");
+  // M = 128 weight rows, K-major e4m3 operands, f32 accumulate; N is added per unit
+  static constexpr uint32_t kIdesc = (1u << 4) | (uint32_t(128 >> 4) << 24);
+};
+
 template <int FMT>
 __device__ __forceinline__ float scale_value(const void* s, int64_t i) {
-  if (FMT == 0) return static_cast<const float*>(s)[i];
-  const uint32_t b = static_cast<const uint8_t*>(s)[i];
+  if (FMT == 0) return __ldg(static_cast<const float*>(s) + i);
+  const uint32_t b = __ldg(static_cast<const uint8_t*>(s) + i);
   return __uint_as_float(b == 0u ? 0x00400000u : b << 23);  // 2^(b - 127)
 }
 
-__device__ __forceinline__ float dot16(const uint4& a, const uint4& b) {
-  const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-  float s = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      __nv_fp8_e4m3 p, q;
-      p.__x = static_cast<__nv_fp8_storage_t>(aw[i] >> (8 * j));
-      q.__x = static_cast<__nv_fp8_storage_t>(bw[i] >> (8 * j));
-      s = fmaf(static_cast<float>(p), static_cast<float>(q), s);
+// The routing as every CTA holds it: pairs sorted by expert (stable), and
+// the expert of each chunk of kChunk pairs.
+struct Routing {
+  uint16_t *list, *cnt, *off, *job, *job_e;
+};
+
+// One warp: counting sort of the P ids by expert.  Returns the chunk count.
+// Lanes with equal ids find each other with a warp match, the lowest one
+// updates the expert's counter, so nothing depends on the order of atomics.
+__device__ __forceinline__ int sort_pairs(const MoeParams& p, const Routing& r) {
+  const int lane = threadIdx.x & 31, P = p.T * p.k;
+  for (int e = lane; e < p.E; e += 32) r.cnt[e] = 0;
+  __syncwarp();
+  bool bad = false;
+  for (int p0 = 0; p0 < P; p0 += 32) {
+    int id = p0 + lane < P ? __ldg(p.ids + p0 + lane) : -1;
+    if (id >= p.E) {
+      bad = true;
+      id = -1;
     }
-  return s;
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, id);
+    if (id >= 0 && (same & ((1u << lane) - 1u)) == 0u) r.cnt[id] = static_cast<uint16_t>(r.cnt[id] + __popc(same));
+    __syncwarp();
+  }
+  if (bad && blockIdx.x == 0) atomicExch(p.status, kInvalidArgStatus);
+  int pairs = 0, jobs = 0;
+  for (int e0 = 0; e0 < p.E; e0 += 32) {
+    const int e = e0 + lane;
+    const int c = e < p.E ? r.cnt[e] : 0, n = (c + kChunk - 1) / kChunk;
+    int sc = c, sn = n;  // inclusive sums over the lanes
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int a = __shfl_up_sync(0xFFFFFFFFu, sc, d), b = __shfl_up_sync(0xFFFFFFFFu, sn, d);
+      if (lane >= d) sc += a, sn += b;
+    }
+    if (e < p.E) {
+      r.off[e] = static_cast<uint16_t>(pairs + sc - c);
+      r.job[e] = static_cast<uint16_t>(jobs + sn - n);
+      for (int q = 0; q < n; ++q) r.job_e[jobs + sn - n + q] = static_cast<uint16_t>(e);
+      r.cnt[e] = 0;  // counted again below
+    }
+    pairs += __shfl_sync(0xFFFFFFFFu, sc, 31);
+    jobs += __shfl_sync(0xFFFFFFFFu, sn, 31);
+  }
+  __syncwarp();
+  for (int p0 = 0; p0 < P; p0 += 32) {
+    int id = p0 + lane < P ? __ldg(p.ids + p0 + lane) : -1;
+    if (id >= p.E) id = -1;
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, id);
+    const uint32_t below = same & ((1u << lane) - 1u);
+    const int at = id >= 0 ? r.cnt[id] : 0;
+    __syncwarp();
+    if (id >= 0) {
+      r.list[r.off[id] + at + __popc(below)] = static_cast<uint16_t>(p0 + lane);
+      if (below == 0u) r.cnt[id] = static_cast<uint16_t>(at + __popc(same));
+    }
+    __syncwarp();
+  }
+  return jobs;
 }
 
-// One weight row times one quantized activation row, by a warp.
-template <int FMT>
-__device__ float row_dot(const uint8_t* w, const void* ws, int64_t ws_row, const uint8_t* xq, const float* xs, int K) {
-  const int lane = threadIdx.x & 31;
-  float acc = 0.0f;
-  for (int k = lane * 16; k < K; k += 512) {
-    const float p = dot16(*reinterpret_cast<const uint4*>(w + k), *reinterpret_cast<const uint4*>(xq + k));
-    acc = fmaf(p, xs[k / 128] * scale_value<FMT>(ws, ws_row + k / 128), acc);
+// This CTA's run of K-blocks, cut into units.
+struct Walk {
+  int64_t w, end, total;
+  int ctas;
+  // the current unit
+  int64_t u;
+  int e, tile, start, m, k0, k1;
+
+  __device__ __forceinline__ Walk(const MoeParams& p, int jobs) {
+    total = static_cast<int64_t>(jobs) * p.tiles * p.Kb;
+    const int64_t most = (total + kMinRun - 1) / kMinRun;
+    ctas = static_cast<int>(most < static_cast<int64_t>(gridDim.x) ? most : static_cast<int64_t>(gridDim.x));
+    w = end = 0;
+    if (static_cast<int>(blockIdx.x) < ctas) {
+      w = begin_of(blockIdx.x);
+      end = begin_of(blockIdx.x + 1);
+    }
+  }
+  __device__ __forceinline__ int64_t begin_of(int64_t cta) const { return cta * total / ctas; }
+  // the CTA whose run holds K-block x: the b with b total / ctas < x + 1 <= (b + 1) total / ctas
+  __device__ __forceinline__ int cta_of(int64_t x) const { return static_cast<int>(((x + 1) * ctas - 1) / total); }
+
+  __device__ __forceinline__ bool next(const MoeParams& p, const Routing& r) {
+    if (w >= end) return false;
+    u = w / p.Kb;
+    k0 = static_cast<int>(w - u * p.Kb);
+    k1 = end - w < p.Kb - k0 ? k0 + static_cast<int>(end - w) : p.Kb;
+    w += k1 - k0;
+    e = r.job_e[u / p.tiles];
+    const int c = r.cnt[e], n = (c + kChunk - 1) / kChunk;
+    const int local = static_cast<int>(u - static_cast<int64_t>(r.job[e]) * p.tiles);
+    tile = local / n;
+    const int q = local - tile * n;
+    start = r.off[e] + q * kChunk;
+    m = c - q * kChunk < kChunk ? c - q * kChunk : kChunk;
+    return true;
+  }
+};
+
+struct Bars {
+  uint64_t *full, *xfull, *empty, *tfull, *tempty, *scfull, *scempty, *teardown, *stall;
+  volatile int *abort_flag, *epi_flag;
+};
+
+__device__ __forceinline__ void moe_raise(const MoeParams& p, const Bars& b) {
+  *b.abort_flag = 1;
+  atomicExch(p.status, kTimeoutStatus);
+}
+
+// First weight rows of a unit's two boxes in the [E * rows, K] matrix.
+template <class C>
+__device__ __forceinline__ int box_row(const MoeParams& p, int e, int tile, int half) {
+  if (C::PHASE == UP) return e * 2 * p.I + half * p.I + tile * 128;
+  return e * p.H + tile * kRowTile + half * 128;
+}
+
+template <class C>
+__device__ __forceinline__ void moe_producer(const CUtensorMap* tmW, const MoeParams& p, const Routing& r, uint8_t* smem,
+                                             const Bars& b, Walk walk) {
+  int64_t it = 0;
+  bool ok = true;
+  while (ok && walk.next(p, r)) {
+    const int row0 = box_row<C>(p, walk.e, walk.tile, 0), row1 = box_row<C>(p, walk.e, walk.tile, 1);
+    for (int kb = walk.k0; kb < walk.k1; ++kb, ++it) {
+      const int slot = static_cast<int>(it % C::STAGES);
+      if (!mbar_wait(b.empty + slot, static_cast<uint32_t>((it / C::STAGES) & 1) ^ 1u, p.wait_limit_ns, b.abort_flag)) {
+        moe_raise(p, b);
+        ok = false;
+        break;
+      }
+      uint8_t* stage = smem + slot * C::kStage;
+      mbar_arrive_expect_tx(b.full + slot, C::kW);
+      tma_load_2d(stage, tmW, b.full + slot, kb * 128, row0);
+      tma_load_2d(stage + 16384, tmW, b.full + slot, kb * 128, row1);
+    }
+  }
+  // every issued copy lands before shared memory goes away
+  for (int64_t i = it > C::STAGES ? it - C::STAGES : 0; i < it; ++i)
+    (void)mbar_wait(b.full + i % C::STAGES, static_cast<uint32_t>((i / C::STAGES) & 1), kDrainNs, nullptr);
+}
+
+template <class C>
+__device__ __forceinline__ void moe_mma(const MoeParams& p, const Routing& r, uint8_t* smem, uint32_t tmem,
+                                        const Bars& b, Walk walk) {
+  bool ok = true;
+  // test hook: a barrier nothing arrives on, so the bounded wait runs out
+  if (p.test_stall && !mbar_wait(b.stall, 0, p.wait_limit_ns, b.abort_flag)) {
+    moe_raise(p, b);
+    ok = false;
+  }
+  uint32_t it = 0;
+  while (ok && walk.next(p, r)) {
+    const uint32_t idesc = C::kIdesc | (uint32_t(walk.m <= 16 ? 2 : 4) << 17);
+    for (int kb = walk.k0; kb < walk.k1; ++kb, ++it) {
+      const uint32_t slot = it % C::STAGES, phase = (it / C::STAGES) & 1u;
+      const uint32_t ab = it % C::kNumAcc, aphase = (it / C::kNumAcc) & 1u;
+      if (!mbar_wait(b.full + slot, phase, p.wait_limit_ns, b.abort_flag) ||
+          !mbar_wait(b.xfull + slot, phase, p.wait_limit_ns, b.abort_flag) ||
+          !mbar_wait(b.tempty + ab, aphase ^ 1u, p.wait_limit_ns, b.abort_flag)) {
+        moe_raise(p, b);
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t a = smem_u32(smem + slot * C::kStage), x = a + C::kW;
+      const uint32_t d = tmem + ab * C::kAccCols;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint64_t bd = smem_desc(x + k * 32, 16, 1024, 2);
+        mma_f8f6f4(d, smem_desc(a + k * 32, 16, 1024, 2), bd, idesc, k > 0 ? 1u : 0u);
+        mma_f8f6f4(d + kChunk, smem_desc(a + 16384 + k * 32, 16, 1024, 2), bd, idesc, k > 0 ? 1u : 0u);
+      }
+      tc_commit(b.empty + slot);
+      tc_commit(b.tfull + ab);
+    }
+  }
+  tc_commit(b.teardown);  // all tensor-core ops done before TMEM is released
+  (void)mbar_wait(b.teardown, 0, kDrainNs, nullptr);
+}
+
+// Warp f of the activation warps takes K-blocks f, f + 4, ... of the run.
+// Eight lanes own one token's 128 channels, four tokens a pass.
+template <class C>
+__device__ __forceinline__ void moe_fill(const MoeParams& p, const Routing& r, uint8_t* smem, const Bars& b, Walk walk) {
+  if (C::PHASE == DOWN) grid_wait_prerequisites();  // h comes from the kernel in front
+  const int fw = (static_cast<int>(threadIdx.x) >> 5) - C::kFillWarp0;
+  const int lane = threadIdx.x & 31, l = lane & 7, r_in = lane >> 3;
+  uint32_t it = 0;
+  while (walk.next(p, r)) {
+    for (int kb = walk.k0; kb < walk.k1; ++kb, ++it) {
+      if (static_cast<int>(it % C::kFillWarps) != fw) continue;
+      const uint32_t slot = it % C::STAGES, ephase = ((it / C::STAGES) & 1u) ^ 1u;
+      const uint32_t ss = it % C::kSlots, sphase = ((it / C::kSlots) & 1u) ^ 1u;
+      uint8_t* xs = smem + slot * C::kStage + C::kW;
+      float* sc = reinterpret_cast<float*>(smem + C::kOffSc) + ss * C::kSlotFloats;
+      // weight scales: lane 0 the first box's, lanes 1 and 2 the second's (its rows may lie in two blocks)
+      float sw = 0.0f;
+      if (lane < 3) {
+        int nb;
+        if (C::PHASE == UP) nb = lane == 0 ? walk.tile : (p.I + walk.tile * 128) / 128 + (lane - 1);
+        else nb = 2 * walk.tile + (lane == 0 ? 0 : 1);
+        if (nb > p.Nb - 1) nb = p.Nb - 1;  // rows past the matrix: never used
+        sw = scale_value<C::FMT>(p.w_scale, (static_cast<int64_t>(walk.e) * p.Nb + nb) * p.Kb + kb);
+      }
+      const int ch = kb * 128 + l * 16;
+      bool waited = false, ok = true;
+      constexpr int kBatch = 4;  // passes whose loads are in flight together
+      for (int c0 = 0; ok && c0 < walk.m; c0 += 4 * kBatch) {
+        uint4 v[kBatch][2];
+        float vs[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int c = c0 + 4 * i + r_in;
+          v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
+          vs[i] = 1.0f;
+          if (c < walk.m) {
+            const int pair = r.list[walk.start + c];
+            if (C::PHASE == DOWN) {
+              if (ch < p.K) v[i][0] = __ldcg(reinterpret_cast<const uint4*>(p.hq + static_cast<int64_t>(pair) * p.I + ch));
+              if (l == 0) vs[i] = __ldcg(p.hs + static_cast<int64_t>(pair) * p.Kb + kb);
+            } else if (C::CODES) {
+              const int t = pair / p.k;
+              if (ch < p.K)
+                v[i][0] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x) + static_cast<int64_t>(t) * p.H + ch);
+              if (l == 0) vs[i] = scale_value<C::FMT>(p.x_scale, static_cast<int64_t>(t) * p.Kb + kb);
+            } else if (ch < p.K) {
+              const int t = pair / p.k;
+              const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) +
+                                                                static_cast<int64_t>(t) * p.ld_x + ch);
+              v[i][0] = src[0];
+              v[i][1] = src[1];
+            }
+          }
+        }
+        if (!waited) {
+          waited = true;
+          if (!mbar_wait_warp(b.empty + slot, ephase, p.wait_limit_ns, b.abort_flag) ||
+              !mbar_wait_warp(b.scempty + ss, sphase, p.wait_limit_ns, b.abort_flag)) {
+            ok = false;
+            break;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          if (c0 + 4 * i >= walk.m) break;
+          const int c = c0 + 4 * i + r_in;
+          uint4 q = v[i][0];
+          float s = vs[i];
+          if (C::PHASE == UP && !C::CODES) {
+            float f[16];
+            {
+              float f0[8], f1[8];
+              unpack_bf16x8(v[i][0], f0);
+              unpack_bf16x8(v[i][1], f1);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                f[j] = f0[j];
+                f[8 + j] = f1[j];
+              }
+            }
+            float amax = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(f[j]));
+            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 4));
+            s = group_scale(amax);
+            const uint32_t sb = C::FMT == 1 ? e8m0_ceil_byte(s) : 0u;
+            q = quantize16<C::FMT>(f, s, sb);
+            if (C::FMT == 1) s = __uint_as_float(sb << 23);
+          }
+          if (c < walk.m) {
+            *reinterpret_cast<uint4*>(xs + (c >> 3) * 1024 + (c & 7) * 128 + ((l ^ (c & 7)) << 4)) = q;
+            if (l == 0) sc[c] = s;
+          }
+        }
+      }
+      if (!ok) {
+        if (lane == 0) moe_raise(p, b);
+        return;
+      }
+      if (lane < 3) sc[kChunk + lane] = sw;
+      fence_proxy_async_smem();  // the tensor core reads what these threads wrote
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(b.xfull + slot);
+        mbar_arrive(b.scfull + ss);
+      }
+    }
+  }
+}
+
+// acc[c] += P[c] * (sx[c] * sw) for one K-block's W columns of both boxes.
+template <int W>
+__device__ __forceinline__ void promote(uint32_t taddr, const float* sc, float sw0, float sw1, float (&acc0)[kChunk],
+                                        float (&acc1)[kChunk]) {
+  uint32_t r0[W], r1[W];
+  if constexpr (W == 16) {
+    tmem_ld_32x32b_x16(taddr, r0);
+    tmem_ld_32x32b_x16(taddr + kChunk, r1);
+    tmem_wait_ld();
+    tmem_reg_fence16(r0);
+    tmem_reg_fence16(r1);
+  } else {
+    tmem_ld_32x32b_x32(taddr, r0);
+    tmem_ld_32x32b_x32(taddr + kChunk, r1);
+    tmem_wait_ld();
+    tmem_reg_fence(r0);
+    tmem_reg_fence(r1);
   }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xFFFFFFFFu, acc, off);
-  return acc;
+  for (int j = 0; j < W; ++j) {
+    const float sx = sc[j];
+    acc0[j] = __fmaf_rn(__uint_as_float(r0[j]), sx * sw0, acc0[j]);
+    acc1[j] = __fmaf_rn(__uint_as_float(r1[j]), sx * sw1, acc1[j]);
+  }
 }
 
-// gate, up, silu, quantization: CTA = (128 rows of I, routed pair).
-template <int FMT>
-__global__ void __launch_bounds__(256) moe_up_kernel(const MoeArgs a, const uint8_t* xq, const void* xs_in,
-                                                     uint8_t* hq, float* hs) {
-  __shared__ float v[128], red[8], xs[kMoeMaxHidden / 128];
-  const int p = blockIdx.y, t = p / a.k, e = a.ids[p];
-  if (e >= a.E && blockIdx.x == 0 && threadIdx.x == 0) atomicExch(reinterpret_cast<uint32_t*>(a.ws), 1u);
-  if (e < 0 || e >= a.E) return;
-  const int Hb = (a.H + 127) / 128, N13b = (2 * a.I + 127) / 128;
-  for (int i = threadIdx.x; i < Hb; i += 256) xs[i] = scale_value<FMT>(xs_in, static_cast<int64_t>(t) * Hb + i);
-  if (threadIdx.x < 128) v[threadIdx.x] = 0.0f;
-  __syncthreads();
-  const int warp = threadIdx.x >> 5;
-  for (int r = warp; r < 128; r += 8) {
-    const int i = blockIdx.x * 128 + r;
-    if (i >= a.I) break;
-    const uint8_t* w = a.w13 + static_cast<int64_t>(e) * 2 * a.I * a.H;
-    const uint8_t* x = xq + static_cast<int64_t>(t) * a.H;
-    const float g = row_dot<FMT>(w + static_cast<int64_t>(i) * a.H, a.s13,
-                                 (static_cast<int64_t>(e) * N13b + i / 128) * Hb, x, xs, a.H);
-    const float u = row_dot<FMT>(w + static_cast<int64_t>(a.I + i) * a.H, a.s13,
-                                 (static_cast<int64_t>(e) * N13b + (a.I + i) / 128) * Hb, x, xs, a.H);
-    if ((threadIdx.x & 31) == 0) v[r] = silu_mul(g, u);
-  }
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    float f[4], amax = 0.0f;
-    for (int j = 0; j < 4; ++j) f[j] = v[threadIdx.x * 4 + j], amax = fmaxf(amax, fabsf(f[j]));
+// UP: silu(gate) * up of a unit's 128 rows, one group per pair: staged
+// [pair][row], then one warp per pair for amax, scale and codes.
+template <class C>
+__device__ __forceinline__ void finish_up(const MoeParams& p, const Routing& r, const Walk& w, float* stage, int et,
+                                          const float (&acc0)[kChunk], const float (&acc1)[kChunk]) {
+  const bool real = w.tile * 128 + et < p.I;
+#pragma unroll
+  for (int c = 0; c < kChunk; ++c)
+    if (c < w.m) stage[c * 128 + et] = real ? silu_mul(acc0[c], acc1[c]) : 0.0f;
+  named_barrier_sync(1, C::kEpiThreads);
+  const int lane = et & 31, i = w.tile * 128 + lane * 4;
+  for (int c = et >> 5; c < w.m; c += 4) {
+    const float4 f = *reinterpret_cast<const float4*>(stage + c * 128 + lane * 4);
+    float amax = fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(f.z), fabsf(f.w)));
+#pragma unroll
     for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
     float s = group_scale(amax);
-    if (FMT == 1) s = __uint_as_float(e8m0_ceil_byte(s) << 23);
-    const int i = blockIdx.x * 128 + threadIdx.x * 4;
-    if (i < a.I)
-      *reinterpret_cast<uint32_t*>(hq + static_cast<int64_t>(p) * a.I + i) =
-          pack_e4m3x4(__fdiv_rn(f[0], s), __fdiv_rn(f[1], s), __fdiv_rn(f[2], s), __fdiv_rn(f[3], s));
-    if (threadIdx.x == 0) hs[static_cast<int64_t>(p) * ((a.I + 127) / 128) + blockIdx.x] = s;
+    if (C::FMT == 1) s = __uint_as_float(e8m0_ceil_byte(s) << 23);
+    const int64_t pair = r.list[w.start + c];
+    if (i < p.I)  // I % 16 == 0: four channels are wholly inside or outside
+      *reinterpret_cast<uint32_t*>(p.hq + pair * p.I + i) =
+          pack_e4m3x4(__fdiv_rn(f.x, s), __fdiv_rn(f.y, s), __fdiv_rn(f.z, s), __fdiv_rn(f.w, s));
+    if (lane == 0) p.hs[pair * ((p.I + 127) / 128) + w.tile] = s;
   }
 }
 
-// down products of one pair: CTA = (128 rows of H, routed pair).
+// The weighted sums over the slots for one row tile, all tokens: one warp per
+// token, eight channels per lane, the slots in order.
+template <class C>
+__device__ __forceinline__ void combine(const MoeParams& p, int tile, int et) {
+  const int n = tile * kRowTile + (et & 31) * 8;
+  if (n >= p.H) return;  // H % 16 == 0
+  for (int t = et >> 5; t < p.T; t += C::kEpiThreads / 32) {
+    float acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+    for (int j0 = 0; j0 < p.k; j0 += 8) {
+      float4 v[8][2];
+      float wt[8];
+      bool on[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int pair = t * p.k + j0 + j;
+        const int id = j0 + j < p.k ? __ldg(p.ids + pair) : -1;
+        on[j] = id >= 0 && id < p.E;
+        if (on[j]) {
+          const float4* src = reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(pair) * p.H + n);
+          wt[j] = __ldg(p.weights + pair);
+          v[j][0] = __ldcg(src);
+          v[j][1] = __ldcg(src + 1);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (!on[j]) continue;
+        acc[0] = fmaf(wt[j], v[j][0].x, acc[0]);
+        acc[1] = fmaf(wt[j], v[j][0].y, acc[1]);
+        acc[2] = fmaf(wt[j], v[j][0].z, acc[2]);
+        acc[3] = fmaf(wt[j], v[j][0].w, acc[3]);
+        acc[4] = fmaf(wt[j], v[j][1].x, acc[4]);
+        acc[5] = fmaf(wt[j], v[j][1].y, acc[5]);
+        acc[6] = fmaf(wt[j], v[j][1].z, acc[6]);
+        acc[7] = fmaf(wt[j], v[j][1].w, acc[7]);
+      }
+    }
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o[i] = static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(acc[2 * i]))) |
+             (static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(acc[2 * i + 1]))) << 16);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + static_cast<int64_t>(t) * p.ld_y + n) =
+        make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+// Counts an arrival on *counter after this CTA's stores; true for every
+// epilogue thread of the CTA that brings it to `want` (which zeroes it for
+// the next call).
+template <class C>
+__device__ __forceinline__ bool arrive_last(uint32_t* counter, uint32_t want, int et, volatile int* flag) {
+  __threadfence();
+  named_barrier_sync(1, C::kEpiThreads);
+  if (et == 0) {
+    const uint32_t done = atomicAdd(counter, 1u) + 1u;
+    *flag = done == want ? 1 : 0;
+    if (done == want) *counter = 0u;
+  }
+  named_barrier_sync(1, C::kEpiThreads);
+  const bool last = *flag != 0;
+  if (last) __threadfence();
+  return last;
+}
+
+template <class C>
+__device__ __forceinline__ void moe_epilogue(const MoeParams& p, const Routing& r, uint8_t* smem, uint32_t tmem,
+                                             const Bars& b, Walk walk, int jobs) {
+  const int warp = static_cast<int>(threadIdx.x) >> 5, lane = threadIdx.x & 31;
+  const int q = warp & 3;          // TMEM lane quadrant
+  const int row = q * 32 + lane;   // weight row inside each box
+  const int et = row;
+  const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+  // row of the second box from which its second scale block starts
+  const int edge = C::PHASE == UP ? 128 - p.I % 128 : 128;
+  float* stage = reinterpret_cast<float*>(smem + C::kOffStage);
+  uint32_t it = 0;
+  while (walk.next(p, r)) {
+    float acc0[kChunk], acc1[kChunk];
+#pragma unroll
+    for (int c = 0; c < kChunk; ++c) acc0[c] = acc1[c] = 0.0f;
+    for (int kb = walk.k0; kb < walk.k1; ++kb, ++it) {
+      const uint32_t ab = it % C::kNumAcc, ss = it % C::kSlots;
+      if (!mbar_wait_warp(b.scfull + ss, (it / C::kSlots) & 1u, p.wait_limit_ns, b.abort_flag) ||
+          !mbar_wait_warp(b.tfull + ab, (it / C::kNumAcc) & 1u, p.wait_limit_ns, b.abort_flag)) {
+        if (lane == 0) moe_raise(p, b);
+        break;
+      }
+      tc_fence_after();
+      const float* sc = reinterpret_cast<const float*>(smem + C::kOffSc) + ss * C::kSlotFloats;
+      const float sw0 = sc[kChunk], sw1 = sc[kChunk + (row < edge ? 1 : 2)];
+      const uint32_t taddr = tmem + lane_base + ab * C::kAccCols;
+      if (walk.m <= 16) promote<16>(taddr, sc, sw0, sw1, acc0, acc1);
+      else promote<32>(taddr, sc, sw0, sw1, acc0, acc1);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(b.tempty + ab);
+        mbar_arrive(b.scempty + ss);
+      }
+    }
+    // one warp that gave up takes all four out together
+    named_barrier_sync(1, C::kEpiThreads);
+    if (et == 0) b.epi_flag[1] = *b.abort_flag;
+    named_barrier_sync(1, C::kEpiThreads);
+    if (b.epi_flag[1]) return;
+
+    if (walk.k0 != 0 || walk.k1 != p.Kb) {  // a cut unit: partial sums, added up by its last CTA
+      const int first = walk.cta_of(walk.u * p.Kb), last = walk.cta_of((walk.u + 1) * p.Kb - 1);
+      float* mine = p.split + (2 * blockIdx.x + (static_cast<int>(blockIdx.x) == first ? 1 : 0)) * kPartFloats;
+#pragma unroll
+      for (int c = 0; c < kChunk; ++c)
+        if (c < walk.m) {
+          __stcg(mine + c * 128 + row, acc0[c]);
+          __stcg(mine + (kChunk + c) * 128 + row, acc1[c]);
+        }
+      if (!arrive_last<C>(p.counters + first, static_cast<uint32_t>(last - first + 1), et, b.epi_flag)) continue;
+#pragma unroll
+      for (int c = 0; c < kChunk; ++c) acc0[c] = acc1[c] = 0.0f;
+      for (int cta = first; cta <= last; ++cta) {
+        const float* part = p.split + (2 * cta + (cta == first ? 1 : 0)) * kPartFloats;
+#pragma unroll
+        for (int c = 0; c < kChunk; ++c)
+          if (c < walk.m) {
+            acc0[c] += __ldcg(part + c * 128 + row);
+            acc1[c] += __ldcg(part + (kChunk + c) * 128 + row);
+          }
+      }
+    }
+    if (C::PHASE == UP) {
+      finish_up<C>(p, r, walk, stage, et, acc0, acc1);
+    } else {
+      const int n = walk.tile * kRowTile + row;
+#pragma unroll
+      for (int c = 0; c < kChunk; ++c)
+        if (c < walk.m) {
+          float* out = p.part + static_cast<int64_t>(r.list[walk.start + c]) * p.H + n;
+          if (n < p.H) __stcg(out, acc0[c]);
+          if (n + 128 < p.H) __stcg(out + 128, acc1[c]);
+        }
+      if (arrive_last<C>(p.counters + kMaxGrid + walk.tile, static_cast<uint32_t>(jobs), et, b.epi_flag))
+        combine<C>(p, walk.tile, et);
+    }
+  }
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, 1)
+    moe_kernel(const __grid_constant__ CUtensorMap tmW, const MoeParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Routing r;
+  r.list = reinterpret_cast<uint16_t*>(smem + C::kOffList);
+  r.cnt = reinterpret_cast<uint16_t*>(smem + C::kOffCnt);
+  r.off = reinterpret_cast<uint16_t*>(smem + C::kOffOff);
+  r.job = reinterpret_cast<uint16_t*>(smem + C::kOffJob);
+  r.job_e = reinterpret_cast<uint16_t*>(smem + C::kOffJobE);
+  Bars b;
+  b.full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  b.xfull = b.full + C::STAGES;
+  b.empty = b.xfull + C::STAGES;
+  b.tfull = b.empty + C::STAGES;
+  b.tempty = b.tfull + C::kNumAcc;
+  b.scfull = b.tempty + C::kNumAcc;
+  b.scempty = b.scfull + C::kSlots;
+  b.teardown = b.scempty + C::kSlots;
+  b.stall = b.teardown + 1;
+  int* words = reinterpret_cast<int*>(b.stall + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(words);
+  b.abort_flag = words + 1;
+  b.epi_flag = words + 2;  // two words
+  int* jobs_slot = words + 4;
+
+  const int warp = static_cast<int>(threadIdx.x) >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&tmW);
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(b.full + s, 1);
+      mbar_init(b.xfull + s, 1);
+      mbar_init(b.empty + s, 1);
+    }
+    for (int a = 0; a < C::kNumAcc; ++a) {
+      mbar_init(b.tfull + a, 1);
+      mbar_init(b.tempty + a, C::kEpiThreads / 32);
+    }
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(b.scfull + s, 1);
+      mbar_init(b.scempty + s, C::kEpiThreads / 32);
+    }
+    mbar_init(b.teardown, 1);
+    mbar_init(b.stall, 1);
+    *b.abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 256);
+    tmem_relinquish();
+  }
+  // UP: everything it reads may come from the kernel in front.  DOWN: that is
+  // UP, which waited itself; only h is new.
+  if (C::PHASE == UP) grid_wait_prerequisites();
+  grid_launch_dependents();
+  if (warp == C::kFillWarp0) {
+    const int jobs = sort_pairs(p, r);
+    if (lane == 0) *jobs_slot = jobs;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int jobs = *jobs_slot;
+  if (jobs > 0) {
+    const Walk walk(p, jobs);
+    if (warp == 0) {
+      if (lane == 0) moe_producer<C>(&tmW, p, r, smem, b, walk);
+    } else if (warp == 1) {
+      if (lane == 0) moe_mma<C>(p, r, smem, tmem, b, walk);
+    } else if (warp < C::kEpiWarp0) {
+      moe_fill<C>(p, r, smem, b, walk);
+    } else {
+      moe_epilogue<C>(p, r, smem, tmem, b, walk, jobs);
+    }
+  } else if (C::PHASE == DOWN && warp >= C::kEpiWarp0) {  // no valid slot at all: zeros
+    grid_wait_prerequisites();
+    for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x)
+      combine<C>(p, tile, static_cast<int>(threadIdx.x) - C::kEpiWarp0 * 32);
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+typedef CUresult (*EncodeTiledFnMoe)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                     const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                     CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFnMoe encode_fn_moe() {
+  // looked up once per process (thread-safe static initialisation)
+  static const EncodeTiledFnMoe fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<EncodeTiledFnMoe>(ptr);
+    return static_cast<EncodeTiledFnMoe>(nullptr);
+  }();
+  return fn;
+}
+
+template <class C>
+cudaError_t launch_phase(const MoeParams& p, const uint8_t* w, int64_t rows, int num_sms, cudaStream_t s) {
+  const EncodeTiledFnMoe fn = encode_fn_moe();
+  if (fn == nullptr) return cudaErrorInvalidValue;
+  CUtensorMap tmW;  // every expert's rows as one e4m3 matrix [rows, K]: 128 x 128 boxes, 128-byte swizzle
+  const cuuint32_t estr[2] = {1, 1}, box[2] = {128, 128};
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.K), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.K)};
+  if (fn(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(w), dims, strides, box, estr,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  auto kern = moe_kernel<C>;
+  // the shared-memory opt-in, once per device
+  static std::atomic<uint64_t> configured{0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = 1ull << (dev & 63);
+  if ((configured.load(std::memory_order_acquire) & bit) == 0) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(num_sms < kMaxGrid ? num_sms : kMaxGrid));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tmW, p);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
 template <int FMT>
-__global__ void __launch_bounds__(256) moe_down_kernel(const MoeArgs a, const uint8_t* hq, const float* hs,
-                                                       float* part) {
-  const int p = blockIdx.y, e = a.ids[p];
-  if (e < 0 || e >= a.E) return;
-  const int Hb = (a.H + 127) / 128, Ib = (a.I + 127) / 128;
-  for (int r = threadIdx.x >> 5; r < 128; r += 8) {
-    const int n = blockIdx.x * 128 + r;
-    if (n >= a.H) break;
-    const float o = row_dot<FMT>(a.w2 + (static_cast<int64_t>(e) * a.H + n) * a.I, a.s2,
-                                 (static_cast<int64_t>(e) * Hb + n / 128) * Ib, hq + static_cast<int64_t>(p) * a.I,
-                                 hs + static_cast<int64_t>(p) * Ib, a.I);
-    if ((threadIdx.x & 31) == 0) part[static_cast<int64_t>(p) * a.H + n] = o;
-  }
-}
-
-__global__ void __launch_bounds__(256) moe_combine_kernel(const MoeArgs a, const float* part) {
-  const int t = blockIdx.y, n = blockIdx.x * 256 + threadIdx.x;
-  if (n >= a.H) return;
-  float acc = 0.0f;
-  for (int j = 0; j < a.k; ++j) {
-    const int e = a.ids[t * a.k + j];
-    if (e >= 0 && e < a.E)
-      acc = fmaf(a.weights[t * a.k + j], part[(static_cast<int64_t>(t) * a.k + j) * a.H + n], acc);
-  }
-  static_cast<__nv_bfloat16*>(a.y)[static_cast<int64_t>(t) * a.ld_y + n] = __float2bfloat16_rn(acc);
+cudaError_t launch_fmt(const MoeArgs& a, const MoeParams& up, const MoeParams& down, int num_sms, cudaStream_t s) {
+  const int64_t rows = static_cast<int64_t>(a.E) * 2 * a.I;
+  const cudaError_t e = a.x_scale != nullptr ? launch_phase<MoeCfg<UP, FMT, true>>(up, a.w13, rows, num_sms, s)
+                                             : launch_phase<MoeCfg<UP, FMT, false>>(up, a.w13, rows, num_sms, s);
+  if (e != cudaSuccess) return e;
+  return launch_phase<MoeCfg<DOWN, FMT, true>>(down, a.w2, static_cast<int64_t>(a.E) * a.H, num_sms, s);
 }
 
 }  // namespace
@@ -152,35 +798,40 @@ size_t moe_workspace_need(int T, int k, int E, int H, int I, int fmt) { return m
 
 cudaError_t launch_moe_mlp(const MoeArgs& a, int fmt, int num_sms, cudaStream_t s) {
   const MoeWs L = moe_ws_layout(a.T, a.k, a.H, a.I);
-  const uint8_t* xq = static_cast<const uint8_t*>(a.x);
-  const void* xs = a.x_scale;
-  if (xs == nullptr) {
-    ActQuantArgs q{};
-    q.x = a.x;
-    q.ld_x = a.ld_x;
-    q.M = a.T;
-    q.K = a.H;
-    q.Kb = (a.H + 127) / 128;
-    q.xq = a.ws + L.xq;
-    q.xs = a.ws + L.xs;
-    q.layout = kScaleRowMajor;
-    if (const cudaError_t e = launch_act_quant(q, fmt, num_sms, s); e != cudaSuccess) return e;
-    xq = a.ws + L.xq;
-    xs = a.ws + L.xs;
-  }
-  uint8_t* hq = a.ws + L.hq;
-  float* hs = reinterpret_cast<float*>(a.ws + L.hs);
-  float* part = reinterpret_cast<float*>(a.ws + L.part);
-  const dim3 up((a.I + 127) / 128, a.T * a.k), down((a.H + 127) / 128, a.T * a.k), comb((a.H + 255) / 256, a.T);
-  if (fmt == 0) {
-    moe_up_kernel<0><<<up, 256, 0, s>>>(a, xq, xs, hq, hs);
-    moe_down_kernel<0><<<down, 256, 0, s>>>(a, hq, hs, part);
-  } else {
-    moe_up_kernel<1><<<up, 256, 0, s>>>(a, xq, xs, hq, hs);
-    moe_down_kernel<1><<<down, 256, 0, s>>>(a, hq, hs, part);
-  }
-  moe_combine_kernel<<<comb, 256, 0, s>>>(a, part);
-  return cudaGetLastError();
+  const int Hb = (a.H + 127) / 128, Ib = (a.I + 127) / 128;
+  MoeParams p{};
+  p.x = a.x;
+  p.ld_x = a.ld_x;
+  p.x_scale = a.x_scale;
+  p.ids = a.ids;
+  p.weights = a.weights;
+  p.T = a.T;
+  p.k = a.k;
+  p.E = a.E;
+  p.H = a.H;
+  p.I = a.I;
+  p.hq = a.ws + L.hq;
+  p.hs = reinterpret_cast<float*>(a.ws + L.hs);
+  p.split = reinterpret_cast<float*>(a.ws + L.split);
+  p.part = reinterpret_cast<float*>(a.ws + L.part);
+  p.y = a.y;
+  p.ld_y = a.ld_y;
+  p.status = reinterpret_cast<uint32_t*>(a.ws);
+  p.counters = reinterpret_cast<uint32_t*>(a.ws + kHeaderCounterOffset);
+  p.wait_limit_ns = a.wait_limit_ns;
+  p.test_stall = a.test_stall;
+  MoeParams up = p, down = p;
+  up.w_scale = a.s13;
+  up.K = a.H;
+  up.Kb = Hb;
+  up.Nb = (2 * a.I + 127) / 128;
+  up.tiles = Ib;
+  down.w_scale = a.s2;
+  down.K = a.I;
+  down.Kb = Ib;
+  down.Nb = Hb;
+  down.tiles = (a.H + kRowTile - 1) / kRowTile;
+  return fmt == 0 ? launch_fmt<0>(a, up, down, num_sms, s) : launch_fmt<1>(a, up, down, num_sms, s);
 }
 
 }  // namespace fg8
