@@ -14,14 +14,14 @@
 //
 // Work: the routed pairs (token, slot) are grouped by expert in chunks of at
 // most 32; chunk and 256-row weight tile (128 gate and the matching 128 up
-// rows, or 256 rows of W2) make a unit of Kb K-blocks of 128.  The units of
-// all chunks in a row (one expert's tiles, its chunks innermost, so that a
-// second chunk finds the tile in L2) are cut into equal runs of K-blocks, one
-// per CTA: every SM streams the same number of bytes whatever the routing is.
-// A unit that a cut divides is added up in CTA order by whichever of its CTAs
+// rows, or 256 rows of W2) make a unit of Kb K-blocks of 128.  All units in a
+// row (tile by tile, the chunks innermost, so that an expert's second chunk
+// finds the tile in L2) are cut into equal runs of K-blocks, one per CTA:
+// every SM streams the same number of bytes whatever the routing is.  A unit
+// that a cut divides is added up in CTA order by whichever of its CTAs
 // finishes last, so the result does not depend on which one that is.
 //
-// Roles (320 threads):
+// Roles (448 threads):
 //   warp 0      producer: per K-block, two TMA boxes of 128 x 128 weights
 //   warp 1      MMA issuer: weights are the tensor core's M side (2 x 128
 //               rows), the chunk's tokens its N side (16 or 32 columns)
@@ -29,12 +29,13 @@
 //               the MMA's B operand (128-byte swizzle), quantized on the way
 //               if x is bf16; their scales and the tile's weight scales into
 //               a ring.  Loads are issued before the ring slot is free.
-//   warps 6-9   epilogue: thread = weight row.  Each K-block's partial
-//               products land in a TMEM buffer of their own and are promoted,
-//               acc += P * (sx * sw), then finished per unit: silu(gate) * up,
-//               the 128-row group's amax, scale and codes (UP); the pair's
-//               products, and by the last unit of a row tile the weighted
-//               sums over the slots (DOWN).
+//   warps 6-13  epilogue: thread = weight row, four warps per box.  Each
+//               K-block's partial products land in a TMEM buffer of their own
+//               (8 of them, which cover the epilogue's end-of-unit work) and
+//               are promoted, acc += P * (sx * sw), then finished per unit:
+//               silu(gate) * up, the 128-row group's amax, scale and codes
+//               (UP); the pairs' products, and by the last CTA of a row tile
+//               the weighted sums over the slots (DOWN).
 //
 // DOWN is launched to overlap UP's end: its first weight tiles are on their
 // way while UP's last units finish; only the warps that read h wait for it.
@@ -120,8 +121,8 @@ struct MoeCfg {
   static constexpr int STAGES = 5;
   static constexpr int kSlots = 8;                       // scale ring
   static constexpr int kSlotFloats = kChunk + 8;
-  static constexpr int kNumAcc = 4, kAccCols = 2 * kChunk;
-  static constexpr int kFillWarp0 = 2, kFillWarps = 4, kEpiWarp0 = 6, kEpiThreads = 128;
+  static constexpr int kNumAcc = 8, kAccCols = 2 * kChunk;
+  static constexpr int kFillWarp0 = 2, kFillWarps = 4, kEpiWarp0 = 6, kEpiThreads = 256;
   static constexpr int kThreads = kEpiWarp0 * 32 + kEpiThreads;
   static constexpr int kOffSc = STAGES * kStage;
   static constexpr int kOffStage = kOffSc + kSlots * kSlotFloats * 4;  // [kChunk][128] float32
@@ -137,6 +138,7 @@ struct MoeCfg {
   static_assert((3 * STAGES + 2 * kNumAcc + 2 * kSlots + 2) * 8 + 32 <= 512, "barrier area");
   static_assert(kSlots % kFillWarps == 0, "a scale slot always belongs to the same warp");
   // M = 128 weight rows, K-major e4m3 operands, f32 accumulate; N is added per unit
+  static_assert(kNumAcc * kAccCols == 512, "TMEM columns");
   static constexpr uint32_t kIdesc = (1u << 4) | (uint32_t(128 >> 4) << 24);
 };
 
@@ -208,15 +210,16 @@ __device__ __forceinline__ int sort_pairs(const MoeParams& p, const Routing& r) 
   return jobs;
 }
 
-// This CTA's run of K-blocks, cut into units.
+// This CTA's run of K-blocks, cut into units: unit u = tile * jobs + job.
 struct Walk {
   int64_t w, end, total;
-  int ctas;
+  int ctas, jobs;
   // the current unit
   int64_t u;
   int e, tile, start, m, k0, k1;
 
-  __device__ __forceinline__ Walk(const MoeParams& p, int jobs) {
+  __device__ __forceinline__ Walk(const MoeParams& p, int njobs) {
+    jobs = njobs;
     total = static_cast<int64_t>(jobs) * p.tiles * p.Kb;
     const int64_t most = (total + kMinRun - 1) / kMinRun;
     ctas = static_cast<int>(most < static_cast<int64_t>(gridDim.x) ? most : static_cast<int64_t>(gridDim.x));
@@ -236,14 +239,17 @@ struct Walk {
     k0 = static_cast<int>(w - u * p.Kb);
     k1 = end - w < p.Kb - k0 ? k0 + static_cast<int>(end - w) : p.Kb;
     w += k1 - k0;
-    e = r.job_e[u / p.tiles];
-    const int c = r.cnt[e], n = (c + kChunk - 1) / kChunk;
-    const int local = static_cast<int>(u - static_cast<int64_t>(r.job[e]) * p.tiles);
-    tile = local / n;
-    const int q = local - tile * n;
+    tile = static_cast<int>(u / jobs);
+    const int job = static_cast<int>(u - static_cast<int64_t>(tile) * jobs);
+    e = r.job_e[job];
+    const int q = job - r.job[e], c = r.cnt[e];
     start = r.off[e] + q * kChunk;
     m = c - q * kChunk < kChunk ? c - q * kChunk : kChunk;
     return true;
+  }
+  // after the current unit: this CTA's run leaves the unit's row tile
+  __device__ __forceinline__ bool leaves_tile(const MoeParams& p) const {
+    return w >= end || w / p.Kb / jobs != tile;
   }
 };
 
@@ -335,6 +341,8 @@ __device__ __forceinline__ void moe_fill(const MoeParams& p, const Routing& r, u
   if (C::PHASE == DOWN) grid_wait_prerequisites();  // h comes from the kernel in front
   const int fw = (static_cast<int>(threadIdx.x) >> 5) - C::kFillWarp0;
   const int lane = threadIdx.x & 31, l = lane & 7, r_in = lane >> 3;
+  // pair / k as a product: pair < 2^12 and k <= 2^5 leave an error below 2^-8
+  const uint32_t inv_k = ((1u << 20) + p.k - 1) / p.k;
   uint32_t it = 0;
   while (walk.next(p, r)) {
     for (int kb = walk.k0; kb < walk.k1; ++kb, ++it) {
@@ -369,12 +377,12 @@ __device__ __forceinline__ void moe_fill(const MoeParams& p, const Routing& r, u
               if (ch < p.K) v[i][0] = __ldcg(reinterpret_cast<const uint4*>(p.hq + static_cast<int64_t>(pair) * p.I + ch));
               if (l == 0) vs[i] = __ldcg(p.hs + static_cast<int64_t>(pair) * p.Kb + kb);
             } else if (C::CODES) {
-              const int t = pair / p.k;
+              const int t = static_cast<int>((static_cast<uint32_t>(pair) * inv_k) >> 20);
               if (ch < p.K)
                 v[i][0] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x) + static_cast<int64_t>(t) * p.H + ch);
               if (l == 0) vs[i] = scale_value<C::FMT>(p.x_scale, static_cast<int64_t>(t) * p.Kb + kb);
             } else if (ch < p.K) {
-              const int t = pair / p.k;
+              const int t = static_cast<int>((static_cast<uint32_t>(pair) * inv_k) >> 20);
               const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) +
                                                                 static_cast<int64_t>(t) * p.ld_x + ch);
               v[i][0] = src[0];
@@ -440,44 +448,51 @@ __device__ __forceinline__ void moe_fill(const MoeParams& p, const Routing& r, u
   }
 }
 
-// acc[c] += P[c] * (sx[c] * sw) for one K-block's W columns of both boxes.
+// acc[c] += P[c] * (sx[c] * sw) for one K-block's W columns of a box.
 template <int W>
-__device__ __forceinline__ void promote(uint32_t taddr, const float* sc, float sw0, float sw1, float (&acc0)[kChunk],
-                                        float (&acc1)[kChunk]) {
-  uint32_t r0[W], r1[W];
+__device__ __forceinline__ void promote(uint32_t taddr, const float* sc, float sw, float (&acc)[kChunk]) {
+  uint32_t r[W];
   if constexpr (W == 16) {
-    tmem_ld_32x32b_x16(taddr, r0);
-    tmem_ld_32x32b_x16(taddr + kChunk, r1);
+    tmem_ld_32x32b_x16(taddr, r);
     tmem_wait_ld();
-    tmem_reg_fence16(r0);
-    tmem_reg_fence16(r1);
+    tmem_reg_fence16(r);
   } else {
-    tmem_ld_32x32b_x32(taddr, r0);
-    tmem_ld_32x32b_x32(taddr + kChunk, r1);
+    tmem_ld_32x32b_x32(taddr, r);
     tmem_wait_ld();
-    tmem_reg_fence(r0);
-    tmem_reg_fence(r1);
+    tmem_reg_fence(r);
   }
 #pragma unroll
-  for (int j = 0; j < W; ++j) {
-    const float sx = sc[j];
-    acc0[j] = __fmaf_rn(__uint_as_float(r0[j]), sx * sw0, acc0[j]);
-    acc1[j] = __fmaf_rn(__uint_as_float(r1[j]), sx * sw1, acc1[j]);
+  for (int j = 0; j < W; j += 4) {
+    const float4 sx = *reinterpret_cast<const float4*>(sc + j);
+    acc[j] = __fmaf_rn(__uint_as_float(r[j]), sx.x * sw, acc[j]);
+    acc[j + 1] = __fmaf_rn(__uint_as_float(r[j + 1]), sx.y * sw, acc[j + 1]);
+    acc[j + 2] = __fmaf_rn(__uint_as_float(r[j + 2]), sx.z * sw, acc[j + 2]);
+    acc[j + 3] = __fmaf_rn(__uint_as_float(r[j + 3]), sx.w * sw, acc[j + 3]);
   }
 }
 
-// UP: silu(gate) * up of a unit's 128 rows, one group per pair: staged
+// UP: silu(gate) * up of a unit's 128 rows, one group per pair: the up half
+// through shared memory to the gate half's threads, the products back as
 // [pair][row], then one warp per pair for amax, scale and codes.
 template <class C>
 __device__ __forceinline__ void finish_up(const MoeParams& p, const Routing& r, const Walk& w, float* stage, int et,
-                                          const float (&acc0)[kChunk], const float (&acc1)[kChunk]) {
-  const bool real = w.tile * 128 + et < p.I;
+                                          const float (&acc)[kChunk]) {
+  const int row = et & 127;
+  if (et >= 128) {
 #pragma unroll
-  for (int c = 0; c < kChunk; ++c)
-    if (c < w.m) stage[c * 128 + et] = real ? silu_mul(acc0[c], acc1[c]) : 0.0f;
+    for (int c = 0; c < kChunk; ++c)
+      if (c < w.m) stage[c * 128 + row] = acc[c];
+  }
+  named_barrier_sync(1, C::kEpiThreads);
+  if (et < 128) {
+    const bool real = w.tile * 128 + row < p.I;
+#pragma unroll
+    for (int c = 0; c < kChunk; ++c)
+      if (c < w.m) stage[c * 128 + row] = real ? silu_mul(acc[c], stage[c * 128 + row]) : 0.0f;
+  }
   named_barrier_sync(1, C::kEpiThreads);
   const int lane = et & 31, i = w.tile * 128 + lane * 4;
-  for (int c = et >> 5; c < w.m; c += 4) {
+  for (int c = et >> 5; c < w.m; c += C::kEpiThreads / 32) {
     const float4 f = *reinterpret_cast<const float4*>(stage + c * 128 + lane * 4);
     float amax = fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(f.z), fabsf(f.w)));
 #pragma unroll
@@ -505,13 +520,13 @@ __device__ __forceinline__ void combine(const MoeParams& p, int tile, int et) {
     for (int j0 = 0; j0 < p.k; j0 += 8) {
       float4 v[8][2];
       float wt[8];
-      bool on[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int pair = t * p.k + j0 + j;
         const int id = j0 + j < p.k ? __ldg(p.ids + pair) : -1;
-        on[j] = id >= 0 && id < p.E;
-        if (on[j]) {
+        wt[j] = 0.0f;
+        v[j][0] = v[j][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (id >= 0 && id < p.E) {
           const float4* src = reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(pair) * p.H + n);
           wt[j] = __ldg(p.weights + pair);
           v[j][0] = __ldcg(src);
@@ -520,7 +535,6 @@ __device__ __forceinline__ void combine(const MoeParams& p, int tile, int et) {
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (!on[j]) continue;
         acc[0] = fmaf(wt[j], v[j][0].x, acc[0]);
         acc[1] = fmaf(wt[j], v[j][0].y, acc[1]);
         acc[2] = fmaf(wt[j], v[j][0].z, acc[2]);
@@ -541,40 +555,71 @@ __device__ __forceinline__ void combine(const MoeParams& p, int tile, int et) {
   }
 }
 
-// Counts an arrival on *counter after this CTA's stores; true for every
-// epilogue thread of the CTA that brings it to `want` (which zeroes it for
-// the next call).
+// Counts an arrival on *counter after this CTA's epilogue stores; true for
+// every epilogue thread of the CTA that brings it to `want` (which zeroes it
+// for the next call).  The barrier orders the threads' stores before the one
+// thread's fence and atomic, and its second fence before their loads.
 template <class C>
 __device__ __forceinline__ bool arrive_last(uint32_t* counter, uint32_t want, int et, volatile int* flag) {
-  __threadfence();
+  if (want == 1u) {
+    named_barrier_sync(1, C::kEpiThreads);
+    return true;
+  }
   named_barrier_sync(1, C::kEpiThreads);
   if (et == 0) {
+    __threadfence();
     const uint32_t done = atomicAdd(counter, 1u) + 1u;
+    __threadfence();
     *flag = done == want ? 1 : 0;
     if (done == want) *counter = 0u;
   }
   named_barrier_sync(1, C::kEpiThreads);
-  const bool last = *flag != 0;
-  if (last) __threadfence();
-  return last;
+  return *flag != 0;
+}
+
+// Sum of a cut unit's partials in CTA order, eight columns and four CTAs in flight.
+__device__ __forceinline__ void sum_partials(const MoeParams& p, int first, int last, int at, int m,
+                                             float (&acc)[kChunk]) {
+#pragma unroll
+  for (int c0 = 0; c0 < kChunk; c0 += 8) {
+    if (c0 >= m) break;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) acc[c0 + c] = 0.0f;
+    for (int cta = first; cta <= last; cta += 4) {
+      float v[4][8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          v[i][c] = cta + i <= last && c0 + c < m
+                        ? __ldcg(p.split + (2 * (cta + i) + (cta + i == first ? 1 : 0)) * kPartFloats +
+                                 (c0 + c) * kRowTile + at)
+                        : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[c0 + c] += v[i][c];
+    }
+  }
 }
 
 template <class C>
 __device__ __forceinline__ void moe_epilogue(const MoeParams& p, const Routing& r, uint8_t* smem, uint32_t tmem,
-                                             const Bars& b, Walk walk, int jobs) {
+                                             const Bars& b, Walk walk) {
   const int warp = static_cast<int>(threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  const int q = warp & 3;          // TMEM lane quadrant
-  const int row = q * 32 + lane;   // weight row inside each box
-  const int et = row;
+  const int q = warp & 3;                           // TMEM lane quadrant
+  const int half = (warp - C::kEpiWarp0) >> 2;      // box
+  const int row = q * 32 + lane;                    // weight row inside the box
+  const int et = half * 128 + row;
   const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
-  // row of the second box from which its second scale block starts
-  const int edge = C::PHASE == UP ? 128 - p.I % 128 : 128;
+  // the box's weight scale: the second box of UP may lie in two scale blocks
+  const int at = kChunk + (half == 0 ? 0 : (C::PHASE == UP && row >= 128 - p.I % 128) ? 2 : 1);
   float* stage = reinterpret_cast<float*>(smem + C::kOffStage);
   uint32_t it = 0;
   while (walk.next(p, r)) {
-    float acc0[kChunk], acc1[kChunk];
+    float acc[kChunk];
 #pragma unroll
-    for (int c = 0; c < kChunk; ++c) acc0[c] = acc1[c] = 0.0f;
+    for (int c = 0; c < kChunk; ++c) acc[c] = 0.0f;
     for (int kb = walk.k0; kb < walk.k1; ++kb, ++it) {
       const uint32_t ab = it % C::kNumAcc, ss = it % C::kSlots;
       if (!mbar_wait_warp(b.scfull + ss, (it / C::kSlots) & 1u, p.wait_limit_ns, b.abort_flag) ||
@@ -584,10 +629,9 @@ __device__ __forceinline__ void moe_epilogue(const MoeParams& p, const Routing& 
       }
       tc_fence_after();
       const float* sc = reinterpret_cast<const float*>(smem + C::kOffSc) + ss * C::kSlotFloats;
-      const float sw0 = sc[kChunk], sw1 = sc[kChunk + (row < edge ? 1 : 2)];
-      const uint32_t taddr = tmem + lane_base + ab * C::kAccCols;
-      if (walk.m <= 16) promote<16>(taddr, sc, sw0, sw1, acc0, acc1);
-      else promote<32>(taddr, sc, sw0, sw1, acc0, acc1);
+      const uint32_t taddr = tmem + lane_base + ab * C::kAccCols + half * kChunk;
+      if (walk.m <= 16) promote<16>(taddr, sc, sc[at], acc);
+      else promote<32>(taddr, sc, sc[at], acc);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -595,46 +639,36 @@ __device__ __forceinline__ void moe_epilogue(const MoeParams& p, const Routing& 
         mbar_arrive(b.scempty + ss);
       }
     }
-    // one warp that gave up takes all four out together
+    // one warp that gave up takes all of them out together
     named_barrier_sync(1, C::kEpiThreads);
     if (et == 0) b.epi_flag[1] = *b.abort_flag;
     named_barrier_sync(1, C::kEpiThreads);
     if (b.epi_flag[1]) return;
 
+    bool whole = true;
     if (walk.k0 != 0 || walk.k1 != p.Kb) {  // a cut unit: partial sums, added up by its last CTA
       const int first = walk.cta_of(walk.u * p.Kb), last = walk.cta_of((walk.u + 1) * p.Kb - 1);
       float* mine = p.split + (2 * blockIdx.x + (static_cast<int>(blockIdx.x) == first ? 1 : 0)) * kPartFloats;
 #pragma unroll
       for (int c = 0; c < kChunk; ++c)
-        if (c < walk.m) {
-          __stcg(mine + c * 128 + row, acc0[c]);
-          __stcg(mine + (kChunk + c) * 128 + row, acc1[c]);
-        }
-      if (!arrive_last<C>(p.counters + first, static_cast<uint32_t>(last - first + 1), et, b.epi_flag)) continue;
-#pragma unroll
-      for (int c = 0; c < kChunk; ++c) acc0[c] = acc1[c] = 0.0f;
-      for (int cta = first; cta <= last; ++cta) {
-        const float* part = p.split + (2 * cta + (cta == first ? 1 : 0)) * kPartFloats;
-#pragma unroll
-        for (int c = 0; c < kChunk; ++c)
-          if (c < walk.m) {
-            acc0[c] += __ldcg(part + c * 128 + row);
-            acc1[c] += __ldcg(part + (kChunk + c) * 128 + row);
-          }
-      }
+        if (c < walk.m) __stcg(mine + c * kRowTile + et, acc[c]);
+      whole = arrive_last<C>(p.counters + first, static_cast<uint32_t>(last - first + 1), et, b.epi_flag);
+      if (whole) sum_partials(p, first, last, et, walk.m, acc);
     }
     if (C::PHASE == UP) {
-      finish_up<C>(p, r, walk, stage, et, acc0, acc1);
-    } else {
-      const int n = walk.tile * kRowTile + row;
+      if (whole) finish_up<C>(p, r, walk, stage, et, acc);
+      continue;
+    }
+    const int n = walk.tile * kRowTile + et;
+    if (whole && n < p.H) {
 #pragma unroll
       for (int c = 0; c < kChunk; ++c)
-        if (c < walk.m) {
-          float* out = p.part + static_cast<int64_t>(r.list[walk.start + c]) * p.H + n;
-          if (n < p.H) __stcg(out, acc0[c]);
-          if (n + 128 < p.H) __stcg(out + 128, acc1[c]);
-        }
-      if (arrive_last<C>(p.counters + kMaxGrid + walk.tile, static_cast<uint32_t>(jobs), et, b.epi_flag))
+        if (c < walk.m) __stcg(p.part + static_cast<int64_t>(r.list[walk.start + c]) * p.H + n, acc[c]);
+    }
+    if (walk.leaves_tile(p)) {  // one arrival per CTA and row tile
+      const int64_t per_tile = static_cast<int64_t>(walk.jobs) * p.Kb;
+      const int first = walk.cta_of(walk.tile * per_tile), last = walk.cta_of((walk.tile + 1) * per_tile - 1);
+      if (arrive_last<C>(p.counters + kMaxGrid + walk.tile, static_cast<uint32_t>(last - first + 1), et, b.epi_flag))
         combine<C>(p, walk.tile, et);
     }
   }
@@ -689,7 +723,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     fence_mbarrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 256);
+    tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
   // UP: everything it reads may come from the kernel in front.  DOWN: that is
@@ -714,7 +748,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     } else if (warp < C::kEpiWarp0) {
       moe_fill<C>(p, r, smem, b, walk);
     } else {
-      moe_epilogue<C>(p, r, smem, tmem, b, walk, jobs);
+      moe_epilogue<C>(p, r, smem, tmem, b, walk);
     }
   } else if (C::PHASE == DOWN && warp >= C::kEpiWarp0) {  // no valid slot at all: zeros
     grid_wait_prerequisites();
@@ -724,7 +758,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 512);
   }
 }
 
