@@ -1126,7 +1126,7 @@ fg8_status fg8_moe_route(const void* logits, int logits_bf16, int64_t T, int64_t
 
 static fg8_status check_moe_shape(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, int fmt) {
   if (!fmt_ok(fmt) || T < 0 || T > kMoeMaxTokens || k <= 0 || k > kMoeMaxTopk || T * k > kMoeMaxPairs || E <= 0 ||
-      E > kMoeMaxExperts || H <= 0 || H > kMoeMaxHidden || I <= 0 || I > kMaxDim / 4)
+      E > kMoeMaxExperts || H <= 0 || H > kMoeMaxHidden || I <= 0 || I > kMoeMaxInner)
     return FG8_ERR_INVALID_ARG;
   if (E * 2 * I + 256 > kMaxDim || E * H + 256 > kMaxDim) return FG8_ERR_INVALID_ARG;
   if (H % 16 != 0 || I % 16 != 0) return FG8_ERR_ALIGNMENT;

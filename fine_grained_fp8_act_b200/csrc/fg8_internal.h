@@ -89,6 +89,7 @@ constexpr int kMoeMaxTopk = 32;
 constexpr int kMoeMaxPairs = 4096;   // tokens x experts per token
 constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeMaxHidden = 16384;
+constexpr int kMoeMaxInner = 1 << 20;
 struct MoeArgs {
   const void* x;       // bf16 [T, H], row stride ld_x; or, with x_scale, e4m3 [T, H]
   int64_t ld_x;

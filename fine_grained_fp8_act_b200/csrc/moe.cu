@@ -16,10 +16,11 @@
 // most 32; chunk and 256-row weight tile (128 gate and the matching 128 up
 // rows, or 256 rows of W2) make a unit of Kb K-blocks of 128.  All units in a
 // row (tile by tile, the chunks innermost, so that an expert's second chunk
-// finds the tile in L2) are cut into equal runs of K-blocks, one per CTA:
-// every SM streams the same number of bytes whatever the routing is.  A unit
-// that a cut divides is added up in CTA order by whichever of its CTAs
-// finishes last, so the result does not depend on which one that is.
+// finds the tile in L2) are dealt out in consecutive runs, one per CTA: whole
+// units where that is even enough, else equal runs of K-blocks, so that every
+// SM streams the same number of bytes whatever the routing is.  A unit that a
+// cut divides is added up in CTA order by whichever of its CTAs finishes
+// last, so the result does not depend on which one that is.
 //
 // Roles (448 threads):
 //   warp 0      producer: per K-block, two TMA boxes of 128 x 128 weights
@@ -27,8 +28,9 @@
 //               rows), the chunk's tokens its N side (16 or 32 columns)
 //   warps 2-5   activations: each K-block's token rows gathered by pair into
 //               the MMA's B operand (128-byte swizzle), quantized on the way
-//               if x is bf16; their scales and the tile's weight scales into
-//               a ring.  Loads are issued before the ring slot is free.
+//               if x is bf16, with their scales and the tile's weight scales.
+//               A ring of its own, deeper than the weights', takes their
+//               latency off the stream; loads go out before a slot is free.
 //   warps 6-13  epilogue: thread = weight row, four warps per box.  Each
 //               K-block's partial products land in a TMEM buffer of their own
 //               (8 of them, which cover the epilogue's end-of-unit work) and
@@ -117,14 +119,14 @@ template <int PHASE_, int FMT_, bool CODES_>
 struct MoeCfg {
   static constexpr int PHASE = PHASE_, FMT = FMT_;
   static constexpr bool CODES = CODES_;  // the activations come as codes and scales
-  static constexpr int kW = 2 * 128 * 128, kX = kChunk * 128, kStage = kW + kX;
-  static constexpr int STAGES = 5;
-  static constexpr int kSlots = 8;                       // scale ring
-  static constexpr int kSlotFloats = kChunk + 8;
-  static constexpr int kNumAcc = 8, kAccCols = 2 * kChunk;
+  static constexpr int kStage = 2 * 128 * 128, STAGES = 5;  // weight ring
+  // slot i of the activation ring, its scales and TMEM buffer i serve the
+  // same K-block, and the epilogue hands all three back together
+  static constexpr int kSlots = 8, kX = kChunk * 128, kSlotFloats = kChunk + 8, kAccCols = 2 * kChunk;
   static constexpr int kFillWarp0 = 2, kFillWarps = 4, kEpiWarp0 = 6, kEpiThreads = 256;
   static constexpr int kThreads = kEpiWarp0 * 32 + kEpiThreads;
-  static constexpr int kOffSc = STAGES * kStage;
+  static constexpr int kOffX = STAGES * kStage;
+  static constexpr int kOffSc = kOffX + kSlots * kX;
   static constexpr int kOffStage = kOffSc + kSlots * kSlotFloats * 4;  // [kChunk][128] float32
   static constexpr int kOffList = kOffStage + kChunk * 128 * 4;        // pairs by expert
   static constexpr int kOffCnt = kOffList + kMoeMaxPairs * 2;          // pairs per expert
@@ -134,11 +136,11 @@ struct MoeCfg {
   static constexpr int kOffBar = (kOffJobE + kMaxJobs * 2 + 15) / 16 * 16;
   static constexpr int kSmem = 1024 + kOffBar + 512;
   static_assert(kSmem <= 232448, "shared memory budget");
-  static_assert(kStage % 1024 == 0, "swizzled operands start on 1024-byte boundaries");
-  static_assert((3 * STAGES + 2 * kNumAcc + 2 * kSlots + 2) * 8 + 32 <= 512, "barrier area");
-  static_assert(kSlots % kFillWarps == 0, "a scale slot always belongs to the same warp");
+  static_assert(kStage % 1024 == 0 && kX % 1024 == 0, "swizzled operands start on 1024-byte boundaries");
+  static_assert((2 * STAGES + 3 * kSlots + 2) * 8 + 32 <= 512, "barrier area");
+  static_assert(kSlots % kFillWarps == 0, "an activation slot always belongs to the same warp");
   // M = 128 weight rows, K-major e4m3 operands, f32 accumulate; N is added per unit
-  static_assert(kNumAcc * kAccCols == 512, "TMEM columns");
+  static_assert(kSlots * kAccCols == 512, "TMEM columns");
   static constexpr uint32_t kIdesc = (1u << 4) | (uint32_t(128 >> 4) << 24);
 };
 
@@ -211,36 +213,62 @@ __device__ __forceinline__ int sort_pairs(const MoeParams& p, const Routing& r) 
 }
 
 // This CTA's run of K-blocks, cut into units: unit u = tile * jobs + job.
+// (total <= kMaxJobs * kMoeMaxInner K-blocks: 32 bits hold it)
 struct Walk {
-  int64_t w, end, total;
+  int left, total, run;  // K-blocks to go, of all CTAs; run: K-blocks per CTA where units stay whole, else 0
   int ctas, jobs;
   // the current unit
-  int64_t u;
-  int e, tile, start, m, k0, k1;
+  int job, e, tile, start, m, k0, k1;
+  int begin;  // first K-block of the next unit
 
   __device__ __forceinline__ Walk(const MoeParams& p, int njobs) {
     jobs = njobs;
-    total = static_cast<int64_t>(jobs) * p.tiles * p.Kb;
-    const int64_t most = (total + kMinRun - 1) / kMinRun;
-    ctas = static_cast<int>(most < static_cast<int64_t>(gridDim.x) ? most : static_cast<int64_t>(gridDim.x));
-    w = end = 0;
+    const int grid = gridDim.x, units = jobs * p.tiles;
+    total = units * p.Kb;
+    // Whole units: the longest run has n of them, and the CTAs beside it
+    // leave it more of the bandwidth (one CTA alone streams a K-block in 0.60
+    // us, all 148 together in 0.73).  Equal runs: total / grid, and putting
+    // the cut units together, about 4 us or 6 K-blocks.  One token over 8
+    // experts (56 K-blocks, 128 + 224 units): 80 us whole, 85 us cut; 2
+    // experts with 8 units of 8 K-blocks: 24 and 22 us.
+    const int n = (units + grid - 1) / grid;
+    run = static_cast<int64_t>(n) * p.Kb * 5 <= (static_cast<int64_t>(total / grid) + 6) * 6 ? n * p.Kb : 0;
+    if (run > 0) {
+      ctas = (units + n - 1) / n;
+    } else {
+      const int most = (total + kMinRun - 1) / kMinRun;
+      ctas = most < grid ? most : grid;
+    }
+    left = 0;
     if (static_cast<int>(blockIdx.x) < ctas) {
-      w = begin_of(blockIdx.x);
-      end = begin_of(blockIdx.x + 1);
+      const int w = begin_of(blockIdx.x);
+      left = begin_of(blockIdx.x + 1) - w;
+      const int u = w / p.Kb;  // the unit before the first, for next() to step from
+      begin = w - u * p.Kb;
+      tile = u / jobs;
+      job = u - tile * jobs - 1;
     }
   }
-  __device__ __forceinline__ int64_t begin_of(int64_t cta) const { return cta * total / ctas; }
-  // the CTA whose run holds K-block x: the b with b total / ctas < x + 1 <= (b + 1) total / ctas
-  __device__ __forceinline__ int cta_of(int64_t x) const { return static_cast<int>(((x + 1) * ctas - 1) / total); }
+  __device__ __forceinline__ int begin_of(int cta) const {
+    if (run > 0) return cta * run < total ? cta * run : total;  // (ctas - 1) * run < total: no overflow
+    return static_cast<int>(static_cast<int64_t>(cta) * total / ctas);
+  }
+  // the CTA whose run holds K-block x: of equal runs the b with b total / ctas < x + 1 <= (b + 1) total / ctas
+  __device__ __forceinline__ int cta_of(int x) const {
+    return run > 0 ? x / run : static_cast<int>((static_cast<int64_t>(x + 1) * ctas - 1) / total);
+  }
+  __device__ __forceinline__ int first_block(const MoeParams& p) const { return (tile * jobs + job) * p.Kb; }
 
   __device__ __forceinline__ bool next(const MoeParams& p, const Routing& r) {
-    if (w >= end) return false;
-    u = w / p.Kb;
-    k0 = static_cast<int>(w - u * p.Kb);
-    k1 = end - w < p.Kb - k0 ? k0 + static_cast<int>(end - w) : p.Kb;
-    w += k1 - k0;
-    tile = static_cast<int>(u / jobs);
-    const int job = static_cast<int>(u - static_cast<int64_t>(tile) * jobs);
+    if (left <= 0) return false;
+    k0 = begin;
+    begin = 0;
+    k1 = left < p.Kb - k0 ? k0 + left : p.Kb;
+    left -= k1 - k0;
+    if (++job == jobs) {
+      job = 0;
+      ++tile;
+    }
     e = r.job_e[job];
     const int q = job - r.job[e], c = r.cnt[e];
     start = r.off[e] + q * kChunk;
@@ -248,13 +276,11 @@ struct Walk {
     return true;
   }
   // after the current unit: this CTA's run leaves the unit's row tile
-  __device__ __forceinline__ bool leaves_tile(const MoeParams& p) const {
-    return w >= end || w / p.Kb / jobs != tile;
-  }
+  __device__ __forceinline__ bool leaves_tile() const { return left <= 0 || job + 1 == jobs; }
 };
 
 struct Bars {
-  uint64_t *full, *xfull, *empty, *tfull, *tempty, *scfull, *scempty, *teardown, *stall;
+  uint64_t *full, *empty, *xfull, *tfull, *tempty, *teardown, *stall;
   volatile int *abort_flag, *epi_flag;
 };
 
@@ -285,7 +311,7 @@ __device__ __forceinline__ void moe_producer(const CUtensorMap* tmW, const MoePa
         break;
       }
       uint8_t* stage = smem + slot * C::kStage;
-      mbar_arrive_expect_tx(b.full + slot, C::kW);
+      mbar_arrive_expect_tx(b.full + slot, C::kStage);
       tma_load_2d(stage, tmW, b.full + slot, kb * 128, row0);
       tma_load_2d(stage + 16384, tmW, b.full + slot, kb * 128, row1);
     }
@@ -309,16 +335,16 @@ __device__ __forceinline__ void moe_mma(const MoeParams& p, const Routing& r, ui
     const uint32_t idesc = C::kIdesc | (uint32_t(walk.m <= 16 ? 2 : 4) << 17);
     for (int kb = walk.k0; kb < walk.k1; ++kb, ++it) {
       const uint32_t slot = it % C::STAGES, phase = (it / C::STAGES) & 1u;
-      const uint32_t ab = it % C::kNumAcc, aphase = (it / C::kNumAcc) & 1u;
-      if (!mbar_wait(b.full + slot, phase, p.wait_limit_ns, b.abort_flag) ||
-          !mbar_wait(b.xfull + slot, phase, p.wait_limit_ns, b.abort_flag) ||
-          !mbar_wait(b.tempty + ab, aphase ^ 1u, p.wait_limit_ns, b.abort_flag)) {
+      // (xfull: its warp waited for the slot's TMEM buffer as well)
+      const uint32_t ab = it % C::kSlots, aphase = (it / C::kSlots) & 1u;
+      if (!mbar_wait(b.xfull + ab, aphase, p.wait_limit_ns, b.abort_flag) ||
+          !mbar_wait(b.full + slot, phase, p.wait_limit_ns, b.abort_flag)) {
         moe_raise(p, b);
         ok = false;
         break;
       }
       tc_fence_after();
-      const uint32_t a = smem_u32(smem + slot * C::kStage), x = a + C::kW;
+      const uint32_t a = smem_u32(smem + slot * C::kStage), x = smem_u32(smem + C::kOffX + ab * C::kX);
       const uint32_t d = tmem + ab * C::kAccCols;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -347,9 +373,8 @@ __device__ __forceinline__ void moe_fill(const MoeParams& p, const Routing& r, u
   while (walk.next(p, r)) {
     for (int kb = walk.k0; kb < walk.k1; ++kb, ++it) {
       if (static_cast<int>(it % C::kFillWarps) != fw) continue;
-      const uint32_t slot = it % C::STAGES, ephase = ((it / C::STAGES) & 1u) ^ 1u;
       const uint32_t ss = it % C::kSlots, sphase = ((it / C::kSlots) & 1u) ^ 1u;
-      uint8_t* xs = smem + slot * C::kStage + C::kW;
+      uint8_t* xs = smem + C::kOffX + ss * C::kX;
       float* sc = reinterpret_cast<float*>(smem + C::kOffSc) + ss * C::kSlotFloats;
       // weight scales: lane 0 the first box's, lanes 1 and 2 the second's (its rows may lie in two blocks)
       float sw = 0.0f;
@@ -392,8 +417,7 @@ __device__ __forceinline__ void moe_fill(const MoeParams& p, const Routing& r, u
         }
         if (!waited) {
           waited = true;
-          if (!mbar_wait_warp(b.empty + slot, ephase, p.wait_limit_ns, b.abort_flag) ||
-              !mbar_wait_warp(b.scempty + ss, sphase, p.wait_limit_ns, b.abort_flag)) {
+          if (!mbar_wait_warp(b.tempty + ss, sphase, p.wait_limit_ns, b.abort_flag)) {
             ok = false;
             break;
           }
@@ -440,10 +464,7 @@ __device__ __forceinline__ void moe_fill(const MoeParams& p, const Routing& r, u
       if (lane < 3) sc[kChunk + lane] = sw;
       fence_proxy_async_smem();  // the tensor core reads what these threads wrote
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(b.xfull + slot);
-        mbar_arrive(b.scfull + ss);
-      }
+      if (lane == 0) mbar_arrive(b.xfull + ss);
     }
   }
 }
@@ -621,23 +642,20 @@ __device__ __forceinline__ void moe_epilogue(const MoeParams& p, const Routing& 
 #pragma unroll
     for (int c = 0; c < kChunk; ++c) acc[c] = 0.0f;
     for (int kb = walk.k0; kb < walk.k1; ++kb, ++it) {
-      const uint32_t ab = it % C::kNumAcc, ss = it % C::kSlots;
-      if (!mbar_wait_warp(b.scfull + ss, (it / C::kSlots) & 1u, p.wait_limit_ns, b.abort_flag) ||
-          !mbar_wait_warp(b.tfull + ab, (it / C::kNumAcc) & 1u, p.wait_limit_ns, b.abort_flag)) {
+      const uint32_t ss = it % C::kSlots, phase = (it / C::kSlots) & 1u;
+      if (!mbar_wait_warp(b.xfull + ss, phase, p.wait_limit_ns, b.abort_flag) ||
+          !mbar_wait_warp(b.tfull + ss, phase, p.wait_limit_ns, b.abort_flag)) {
         if (lane == 0) moe_raise(p, b);
         break;
       }
       tc_fence_after();
       const float* sc = reinterpret_cast<const float*>(smem + C::kOffSc) + ss * C::kSlotFloats;
-      const uint32_t taddr = tmem + lane_base + ab * C::kAccCols + half * kChunk;
+      const uint32_t taddr = tmem + lane_base + ss * C::kAccCols + half * kChunk;
       if (walk.m <= 16) promote<16>(taddr, sc, sc[at], acc);
       else promote<32>(taddr, sc, sc[at], acc);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(b.tempty + ab);
-        mbar_arrive(b.scempty + ss);
-      }
+      if (lane == 0) mbar_arrive(b.tempty + ss);
     }
     // one warp that gave up takes all of them out together
     named_barrier_sync(1, C::kEpiThreads);
@@ -647,7 +665,7 @@ __device__ __forceinline__ void moe_epilogue(const MoeParams& p, const Routing& 
 
     bool whole = true;
     if (walk.k0 != 0 || walk.k1 != p.Kb) {  // a cut unit: partial sums, added up by its last CTA
-      const int first = walk.cta_of(walk.u * p.Kb), last = walk.cta_of((walk.u + 1) * p.Kb - 1);
+      const int b0 = walk.first_block(p), first = walk.cta_of(b0), last = walk.cta_of(b0 + p.Kb - 1);
       float* mine = p.split + (2 * blockIdx.x + (static_cast<int>(blockIdx.x) == first ? 1 : 0)) * kPartFloats;
 #pragma unroll
       for (int c = 0; c < kChunk; ++c)
@@ -665,8 +683,8 @@ __device__ __forceinline__ void moe_epilogue(const MoeParams& p, const Routing& 
       for (int c = 0; c < kChunk; ++c)
         if (c < walk.m) __stcg(p.part + static_cast<int64_t>(r.list[walk.start + c]) * p.H + n, acc[c]);
     }
-    if (walk.leaves_tile(p)) {  // one arrival per CTA and row tile
-      const int64_t per_tile = static_cast<int64_t>(walk.jobs) * p.Kb;
+    if (walk.leaves_tile()) {  // one arrival per CTA and row tile
+      const int per_tile = walk.jobs * p.Kb;
       const int first = walk.cta_of(walk.tile * per_tile), last = walk.cta_of((walk.tile + 1) * per_tile - 1);
       if (arrive_last<C>(p.counters + kMaxGrid + walk.tile, static_cast<uint32_t>(last - first + 1), et, b.epi_flag))
         combine<C>(p, walk.tile, et);
@@ -687,13 +705,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   r.job_e = reinterpret_cast<uint16_t*>(smem + C::kOffJobE);
   Bars b;
   b.full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  b.xfull = b.full + C::STAGES;
-  b.empty = b.xfull + C::STAGES;
-  b.tfull = b.empty + C::STAGES;
-  b.tempty = b.tfull + C::kNumAcc;
-  b.scfull = b.tempty + C::kNumAcc;
-  b.scempty = b.scfull + C::kSlots;
-  b.teardown = b.scempty + C::kSlots;
+  b.empty = b.full + C::STAGES;
+  b.xfull = b.empty + C::STAGES;
+  b.tfull = b.xfull + C::kSlots;
+  b.tempty = b.tfull + C::kSlots;
+  b.teardown = b.tempty + C::kSlots;
   b.stall = b.teardown + 1;
   int* words = reinterpret_cast<int*>(b.stall + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(words);
@@ -706,16 +722,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     prefetch_tmap(&tmW);
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(b.full + s, 1);
-      mbar_init(b.xfull + s, 1);
       mbar_init(b.empty + s, 1);
     }
-    for (int a = 0; a < C::kNumAcc; ++a) {
-      mbar_init(b.tfull + a, 1);
-      mbar_init(b.tempty + a, C::kEpiThreads / 32);
-    }
     for (int s = 0; s < C::kSlots; ++s) {
-      mbar_init(b.scfull + s, 1);
-      mbar_init(b.scempty + s, C::kEpiThreads / 32);
+      mbar_init(b.xfull + s, 1);
+      mbar_init(b.tfull + s, 1);
+      mbar_init(b.tempty + s, C::kEpiThreads / 32);
     }
     mbar_init(b.teardown, 1);
     mbar_init(b.stall, 1);
