@@ -22,16 +22,16 @@
 // cut divides is added up in CTA order by whichever of its CTAs finishes
 // last, so the result does not depend on which one that is.
 //
-// Roles (448 threads):
+// Roles (512 threads):
 //   warp 0      producer: per K-block, two TMA boxes of 128 x 128 weights
 //   warp 1      MMA issuer: weights are the tensor core's M side (2 x 128
 //               rows), the chunk's tokens its N side (16 or 32 columns)
-//   warps 2-5   activations: each K-block's token rows gathered by pair into
+//   warps 2-7   activations: each K-block's token rows gathered by pair into
 //               the MMA's B operand (128-byte swizzle), quantized on the way
 //               if x is bf16, with their scales and the tile's weight scales.
 //               A ring of its own, deeper than the weights', takes their
 //               latency off the stream; loads go out before a slot is free.
-//   warps 6-13  epilogue: thread = weight row, four warps per box.  Each
+//   warps 8-15  epilogue: thread = weight row, four warps per box.  Each
 //               K-block's partial products land in a TMEM buffer of their own
 //               (8 of them, which cover the epilogue's end-of-unit work) and
 //               are promoted, acc += P * (sx * sw), then finished per unit:
@@ -123,12 +123,13 @@ struct MoeCfg {
   // slot i of the activation ring, its scales and TMEM buffer i serve the
   // same K-block, and the epilogue hands all three back together
   static constexpr int kSlots = 8, kX = kChunk * 128, kSlotFloats = kChunk + 8, kAccCols = 2 * kChunk;
-  static constexpr int kFillWarp0 = 2, kFillWarps = 4, kEpiWarp0 = 6, kEpiThreads = 256;
+  static constexpr int kFillWarp0 = 2, kFillWarps = 6, kEpiWarp0 = 8, kEpiThreads = 256;
   static constexpr int kThreads = kEpiWarp0 * 32 + kEpiThreads;
   static constexpr int kOffX = STAGES * kStage;
   static constexpr int kOffSc = kOffX + kSlots * kX;
-  static constexpr int kOffStage = kOffSc + kSlots * kSlotFloats * 4;  // [kChunk][128] float32
-  static constexpr int kOffList = kOffStage + kChunk * 128 * 4;        // pairs by expert
+  static constexpr int kStagePairs = 16;
+  static constexpr int kOffStage = kOffSc + kSlots * kSlotFloats * 4;     // [2][kStagePairs][128] float32
+  static constexpr int kOffList = kOffStage + 2 * kStagePairs * 128 * 4;  // pairs by expert
   static constexpr int kOffCnt = kOffList + kMoeMaxPairs * 2;          // pairs per expert
   static constexpr int kOffOff = kOffCnt + kMoeMaxExperts * 2;         // first pair
   static constexpr int kOffJob = kOffOff + kMoeMaxExperts * 2;         // first chunk
@@ -138,7 +139,6 @@ struct MoeCfg {
   static_assert(kSmem <= 232448, "shared memory budget");
   static_assert(kStage % 1024 == 0 && kX % 1024 == 0, "swizzled operands start on 1024-byte boundaries");
   static_assert((2 * STAGES + 3 * kSlots + 2) * 8 + 32 <= 512, "barrier area");
-  static_assert(kSlots % kFillWarps == 0, "an activation slot always belongs to the same warp");
   // M = 128 weight rows, K-major e4m3 operands, f32 accumulate; N is added per unit
   static_assert(kSlots * kAccCols == 512, "TMEM columns");
   static constexpr uint32_t kIdesc = (1u << 4) | (uint32_t(128 >> 4) << 24);
@@ -296,6 +296,13 @@ __device__ __forceinline__ int box_row(const MoeParams& p, int e, int tile, int 
   return e * p.H + tile * kRowTile + half * 128;
 }
 
+// DOWN's last tile may end inside its first box: the second is not loaded
+// then, and what the MMA makes of the stage's old bytes is never stored.
+template <class C>
+__device__ __forceinline__ bool has_second(const MoeParams& p, int tile) {
+  return C::PHASE == UP || tile * kRowTile + 128 < p.H;
+}
+
 template <class C>
 __device__ __forceinline__ void moe_producer(const CUtensorMap* tmW, const MoeParams& p, const Routing& r, uint8_t* smem,
                                              const Bars& b, Walk walk) {
@@ -303,6 +310,7 @@ __device__ __forceinline__ void moe_producer(const CUtensorMap* tmW, const MoePa
   bool ok = true;
   while (ok && walk.next(p, r)) {
     const int row0 = box_row<C>(p, walk.e, walk.tile, 0), row1 = box_row<C>(p, walk.e, walk.tile, 1);
+    const bool second = has_second<C>(p, walk.tile);
     for (int kb = walk.k0; kb < walk.k1; ++kb, ++it) {
       const int slot = static_cast<int>(it % C::STAGES);
       if (!mbar_wait(b.empty + slot, static_cast<uint32_t>((it / C::STAGES) & 1) ^ 1u, p.wait_limit_ns, b.abort_flag)) {
@@ -311,9 +319,9 @@ __device__ __forceinline__ void moe_producer(const CUtensorMap* tmW, const MoePa
         break;
       }
       uint8_t* stage = smem + slot * C::kStage;
-      mbar_arrive_expect_tx(b.full + slot, C::kStage);
+      mbar_arrive_expect_tx(b.full + slot, second ? C::kStage : C::kStage / 2);
       tma_load_2d(stage, tmW, b.full + slot, kb * 128, row0);
-      tma_load_2d(stage + 16384, tmW, b.full + slot, kb * 128, row1);
+      if (second) tma_load_2d(stage + 16384, tmW, b.full + slot, kb * 128, row1);
     }
   }
   // every issued copy lands before shared memory goes away
@@ -360,7 +368,7 @@ __device__ __forceinline__ void moe_mma(const MoeParams& p, const Routing& r, ui
   (void)mbar_wait(b.teardown, 0, kDrainNs, nullptr);
 }
 
-// Warp f of the activation warps takes K-blocks f, f + 4, ... of the run.
+// Warp f of the activation warps takes K-blocks f, f + kFillWarps, ... of the run.
 // Eight lanes own one token's 128 channels, four tokens a pass.
 template <class C>
 __device__ __forceinline__ void moe_fill(const MoeParams& p, const Routing& r, uint8_t* smem, const Bars& b, Walk walk) {
@@ -492,39 +500,83 @@ __device__ __forceinline__ void promote(uint32_t taddr, const float* sc, float s
   }
 }
 
-// UP: silu(gate) * up of a unit's 128 rows, one group per pair: the up half
-// through shared memory to the gate half's threads, the products back as
-// [pair][row], then one warp per pair for amax, scale and codes.
+// Sum of a cut unit's partials at (column, row of the thread), in CTA order.
+struct CutUnit {
+  int first, last;  // its CTAs
+  __device__ __forceinline__ const float* part(const MoeParams& p, int cta) const {
+    return p.split + (2 * cta + (cta == first ? 1 : 0)) * kPartFloats;
+  }
+  // columns c .. c + 3; 16 loads in flight
+  __device__ __forceinline__ float4 sum4(const MoeParams& p, int c, int m, int et) const {
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int cta = first; cta <= last; cta += 4) {
+      float v[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          v[i][j] = cta + i <= last && c + j < m ? __ldcg(part(p, cta + i) + (c + j) * kRowTile + et) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[j] += v[i][j];
+    }
+    return make_float4(s[0], s[1], s[2], s[3]);
+  }
+};
+
+// UP: silu(gate) * up of a unit's 128 rows, one group per pair: both halves
+// through shared memory ([box][pair][row], 16 pairs at a time), then one warp
+// per pair for the products, amax, scale and codes.  Only the stores from the
+// accumulators are unrolled: this code runs once per unit, and unrolled as a
+// whole it spent more time on instruction fetches than on work (a unit's end
+// took 4 to 6 us).
 template <class C>
 __device__ __forceinline__ void finish_up(const MoeParams& p, const Routing& r, const Walk& w, float* stage, int et,
-                                          const float (&acc)[kChunk]) {
-  const int row = et & 127;
-  if (et >= 128) {
-#pragma unroll
-    for (int c = 0; c < kChunk; ++c)
-      if (c < w.m) stage[c * 128 + row] = acc[c];
-  }
-  named_barrier_sync(1, C::kEpiThreads);
-  if (et < 128) {
-    const bool real = w.tile * 128 + row < p.I;
-#pragma unroll
-    for (int c = 0; c < kChunk; ++c)
-      if (c < w.m) stage[c * 128 + row] = real ? silu_mul(acc[c], stage[c * 128 + row]) : 0.0f;
-  }
-  named_barrier_sync(1, C::kEpiThreads);
+                                          const float (&acc)[kChunk], bool cut, const CutUnit& cu) {
+  float* mine = stage + (et >> 7) * (C::kStagePairs * 128) + (et & 127);
   const int lane = et & 31, i = w.tile * 128 + lane * 4;
-  for (int c = et >> 5; c < w.m; c += C::kEpiThreads / 32) {
-    const float4 f = *reinterpret_cast<const float4*>(stage + c * 128 + lane * 4);
-    float amax = fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(f.z), fabsf(f.w)));
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
-    float s = group_scale(amax);
-    if (C::FMT == 1) s = __uint_as_float(e8m0_ceil_byte(s) << 23);
-    const int64_t pair = r.list[w.start + c];
-    if (i < p.I)  // I % 16 == 0: four channels are wholly inside or outside
-      *reinterpret_cast<uint32_t*>(p.hq + pair * p.I + i) =
-          pack_e4m3x4(__fdiv_rn(f.x, s), __fdiv_rn(f.y, s), __fdiv_rn(f.z, s), __fdiv_rn(f.w, s));
-    if (lane == 0) p.hs[pair * ((p.I + 127) / 128) + w.tile] = s;
+  for (int c0 = 0; c0 < kChunk; c0 += C::kStagePairs) {
+    if (c0 >= w.m) break;
+    const int n = w.m - c0 < C::kStagePairs ? w.m - c0 : C::kStagePairs;
+    named_barrier_sync(1, C::kEpiThreads);  // the stage's last readers are done
+    if (cut) {
+#pragma unroll 1
+      for (int c = 0; c < n; c += 4) {
+        const float4 v = cu.sum4(p, c0 + c, w.m, et);
+        mine[c * 128] = v.x;
+        mine[(c + 1) * 128] = v.y;
+        mine[(c + 2) * 128] = v.z;
+        mine[(c + 3) * 128] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < C::kStagePairs; ++c)
+        if (c < n) mine[c * 128] = acc[c0 + c];
+    }
+    named_barrier_sync(1, C::kEpiThreads);
+#pragma unroll 1
+    for (int c = et >> 5; c < n; c += C::kEpiThreads / 32) {
+      const float4 g = *reinterpret_cast<const float4*>(stage + c * 128 + lane * 4);
+      const float4 u = *reinterpret_cast<const float4*>(stage + (C::kStagePairs + c) * 128 + lane * 4);
+      float f[4] = {silu_mul(g.x, u.x), silu_mul(g.y, u.y), silu_mul(g.z, u.z), silu_mul(g.w, u.w)};
+      float amax = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (i >= p.I) f[j] = 0.0f;  // I % 16 == 0: four channels are wholly inside or outside
+        amax = fmaxf(amax, fabsf(f[j]));
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
+      float s = group_scale(amax);
+      if (C::FMT == 1) s = __uint_as_float(e8m0_ceil_byte(s) << 23);
+      const int64_t pair = r.list[w.start + c0 + c];
+      if (i < p.I)
+        *reinterpret_cast<uint32_t*>(p.hq + pair * p.I + i) =
+            pack_e4m3x4(__fdiv_rn(f[0], s), __fdiv_rn(f[1], s), __fdiv_rn(f[2], s), __fdiv_rn(f[3], s));
+      if (lane == 0) p.hs[pair * ((p.I + 127) / 128) + w.tile] = s;
+    }
   }
 }
 
@@ -598,32 +650,6 @@ __device__ __forceinline__ bool arrive_last(uint32_t* counter, uint32_t want, in
   return *flag != 0;
 }
 
-// Sum of a cut unit's partials in CTA order, eight columns and four CTAs in flight.
-__device__ __forceinline__ void sum_partials(const MoeParams& p, int first, int last, int at, int m,
-                                             float (&acc)[kChunk]) {
-#pragma unroll
-  for (int c0 = 0; c0 < kChunk; c0 += 8) {
-    if (c0 >= m) break;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) acc[c0 + c] = 0.0f;
-    for (int cta = first; cta <= last; cta += 4) {
-      float v[4][8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          v[i][c] = cta + i <= last && c0 + c < m
-                        ? __ldcg(p.split + (2 * (cta + i) + (cta + i == first ? 1 : 0)) * kPartFloats +
-                                 (c0 + c) * kRowTile + at)
-                        : 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int c = 0; c < 8; ++c) acc[c0 + c] += v[i][c];
-    }
-  }
-}
-
 template <class C>
 __device__ __forceinline__ void moe_epilogue(const MoeParams& p, const Routing& r, uint8_t* smem, uint32_t tmem,
                                              const Bars& b, Walk walk) {
@@ -637,15 +663,19 @@ __device__ __forceinline__ void moe_epilogue(const MoeParams& p, const Routing& 
   const int at = kChunk + (half == 0 ? 0 : (C::PHASE == UP && row >= 128 - p.I % 128) ? 2 : 1);
   float* stage = reinterpret_cast<float*>(smem + C::kOffStage);
   uint32_t it = 0;
+  bool ok = true;
   while (walk.next(p, r)) {
     float acc[kChunk];
 #pragma unroll
     for (int c = 0; c < kChunk; ++c) acc[c] = 0.0f;
-    for (int kb = walk.k0; kb < walk.k1; ++kb, ++it) {
+    for (int kb = walk.k0; ok && kb < walk.k1; ++kb, ++it) {
       const uint32_t ss = it % C::kSlots, phase = (it / C::kSlots) & 1u;
       if (!mbar_wait_warp(b.xfull + ss, phase, p.wait_limit_ns, b.abort_flag) ||
           !mbar_wait_warp(b.tfull + ss, phase, p.wait_limit_ns, b.abort_flag)) {
+        // from here on this warp only keeps its barriers (every warp's next
+        // wait fails likewise); what it stores is unspecified, in bounds
         if (lane == 0) moe_raise(p, b);
+        ok = false;
         break;
       }
       tc_fence_after();
@@ -657,31 +687,41 @@ __device__ __forceinline__ void moe_epilogue(const MoeParams& p, const Routing& 
       __syncwarp();
       if (lane == 0) mbar_arrive(b.tempty + ss);
     }
-    // one warp that gave up takes all of them out together
-    named_barrier_sync(1, C::kEpiThreads);
-    if (et == 0) b.epi_flag[1] = *b.abort_flag;
-    named_barrier_sync(1, C::kEpiThreads);
-    if (b.epi_flag[1]) return;
-
+    const bool cut = walk.k0 != 0 || walk.k1 != p.Kb;
     bool whole = true;
-    if (walk.k0 != 0 || walk.k1 != p.Kb) {  // a cut unit: partial sums, added up by its last CTA
-      const int b0 = walk.first_block(p), first = walk.cta_of(b0), last = walk.cta_of(b0 + p.Kb - 1);
-      float* mine = p.split + (2 * blockIdx.x + (static_cast<int>(blockIdx.x) == first ? 1 : 0)) * kPartFloats;
+    CutUnit cu{0, 0};
+    if (cut) {  // partial sums, added up by the last of the unit's CTAs
+      const int b0 = walk.first_block(p);
+      cu.first = walk.cta_of(b0);
+      cu.last = walk.cta_of(b0 + p.Kb - 1);
+      float* mine = p.split + (2 * blockIdx.x + (static_cast<int>(blockIdx.x) == cu.first ? 1 : 0)) * kPartFloats;
 #pragma unroll
       for (int c = 0; c < kChunk; ++c)
         if (c < walk.m) __stcg(mine + c * kRowTile + et, acc[c]);
-      whole = arrive_last<C>(p.counters + first, static_cast<uint32_t>(last - first + 1), et, b.epi_flag);
-      if (whole) sum_partials(p, first, last, et, walk.m, acc);
+      whole = arrive_last<C>(p.counters + cu.first, static_cast<uint32_t>(cu.last - cu.first + 1), et, b.epi_flag);
     }
     if (C::PHASE == UP) {
-      if (whole) finish_up<C>(p, r, walk, stage, et, acc);
+      if (whole) finish_up<C>(p, r, walk, stage, et, acc, cut, cu);
       continue;
     }
     const int n = walk.tile * kRowTile + et;
     if (whole && n < p.H) {
+      float* out = p.part + n;
+      const uint16_t* pairs = r.list + walk.start;
+      if (cut) {
+#pragma unroll 1
+        for (int c = 0; c < walk.m; c += 4) {
+          const float4 v = cu.sum4(p, c, walk.m, et);
+          __stcg(out + static_cast<int64_t>(pairs[c]) * p.H, v.x);
+          if (c + 1 < walk.m) __stcg(out + static_cast<int64_t>(pairs[c + 1]) * p.H, v.y);
+          if (c + 2 < walk.m) __stcg(out + static_cast<int64_t>(pairs[c + 2]) * p.H, v.z);
+          if (c + 3 < walk.m) __stcg(out + static_cast<int64_t>(pairs[c + 3]) * p.H, v.w);
+        }
+      } else {
 #pragma unroll
-      for (int c = 0; c < kChunk; ++c)
-        if (c < walk.m) __stcg(p.part + static_cast<int64_t>(r.list[walk.start + c]) * p.H + n, acc[c]);
+        for (int c = 0; c < kChunk; ++c)
+          if (c < walk.m) __stcg(out + static_cast<int64_t>(pairs[c]) * p.H, acc[c]);
+      }
     }
     if (walk.leaves_tile()) {  // one arrival per CTA and row tile
       const int per_tile = walk.jobs * p.Kb;
@@ -714,8 +754,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   int* words = reinterpret_cast<int*>(b.stall + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(words);
   b.abort_flag = words + 1;
-  b.epi_flag = words + 2;  // two words
-  int* jobs_slot = words + 4;
+  b.epi_flag = words + 2;
+  int* jobs_slot = words + 3;
 
   const int warp = static_cast<int>(threadIdx.x) >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
