@@ -130,11 +130,15 @@ struct MoeCfg {
   static constexpr int kStagePairs = 16;
   static constexpr int kOffStage = kOffSc + kSlots * kSlotFloats * 4;     // [2][kStagePairs][128] float32
   static constexpr int kOffList = kOffStage + 2 * kStagePairs * 128 * 4;  // pairs by expert
-  static constexpr int kOffCnt = kOffList + kMoeMaxPairs * 2;          // pairs per expert
-  static constexpr int kOffOff = kOffCnt + kMoeMaxExperts * 2;         // first pair
-  static constexpr int kOffJob = kOffOff + kMoeMaxExperts * 2;         // first chunk
-  static constexpr int kOffJobE = kOffJob + kMoeMaxExperts * 2;        // expert of each chunk
-  static constexpr int kOffBar = (kOffJobE + kMaxJobs * 2 + 15) / 16 * 16;
+  static constexpr int kOffOff = kOffList + kMoeMaxPairs * 2;             // first pair of each expert
+  static constexpr int kOffJob = kOffOff + kMoeMaxExperts * 2;            // its first chunk
+  static constexpr int kOffJobE = kOffJob + kMoeMaxExperts * 2;           // expert of each chunk
+  static constexpr int kOffCnt = (kOffJobE + kMaxJobs * 2 + 15) / 16 * 16;  // pairs per expert
+  static constexpr int kOffBar = kOffCnt + kMoeMaxExperts * 2;
+  // while the pairs are sorted, before anything is staged
+  static constexpr int kOffCount = kOffX, kOffIds = kOffCount + kMoeMaxExperts * 4;
+  static constexpr int kOffNext = kOffIds + kMoeMaxPairs * 2;
+  static_assert(kOffNext + kMoeMaxExperts * 2 <= kOffSc, "sort scratch");
   static constexpr int kSmem = 1024 + kOffBar + 512;
   static_assert(kSmem <= 232448, "shared memory budget");
   static_assert(kStage % 1024 == 0 && kX % 1024 == 0, "swizzled operands start on 1024-byte boundaries");
@@ -155,61 +159,66 @@ __device__ __forceinline__ float scale_value(const void* s, int64_t i) {
 // the expert of each chunk of kChunk pairs.
 struct Routing {
   uint16_t *list, *cnt, *off, *job, *job_e;
+  uint32_t* count;      // scratch of the sort, as ids and next
+  uint16_t *ids, *next;
 };
 
-// One warp: counting sort of the P ids by expert.  Returns the chunk count.
-// Lanes with equal ids find each other with a warp match, the lowest one
-// updates the expert's counter, so nothing depends on the order of atomics.
-__device__ __forceinline__ int sort_pairs(const MoeParams& p, const Routing& r) {
+// Counting sort of the P ids by expert, in three steps with a block barrier
+// after each of the first two: every thread counts its ids (integer atomics:
+// the counts do not depend on their order); one warp makes the prefix sums;
+// and places the pairs in their order, lanes with equal ids finding each
+// other with a warp match.
+__device__ __forceinline__ void count_pairs(const MoeParams& p, const Routing& r) {
+  const int P = p.T * p.k;
+  for (int i = threadIdx.x; i < P; i += blockDim.x) {
+    const int id = __ldg(p.ids + i);
+    const bool on = id >= 0 && id < p.E;
+    r.ids[i] = on ? static_cast<uint16_t>(id) : static_cast<uint16_t>(0xFFFFu);
+    if (on) atomicAdd(r.count + id, 1u);
+    else if (id >= 0 && blockIdx.x == 0) atomicExch(p.status, kInvalidArgStatus);
+  }
+}
+
+__device__ __forceinline__ int place_pairs(const MoeParams& p, const Routing& r) {
   const int lane = threadIdx.x & 31, P = p.T * p.k;
-  for (int e = lane; e < p.E; e += 32) r.cnt[e] = 0;
-  __syncwarp();
-  bool bad = false;
-  for (int p0 = 0; p0 < P; p0 += 32) {
-    int id = p0 + lane < P ? __ldg(p.ids + p0 + lane) : -1;
-    if (id >= p.E) {
-      bad = true;
-      id = -1;
-    }
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, id);
-    if (id >= 0 && (same & ((1u << lane) - 1u)) == 0u) r.cnt[id] = static_cast<uint16_t>(r.cnt[id] + __popc(same));
-    __syncwarp();
+  const int per = (p.E + 31) / 32, e0 = lane * per, e1 = e0 + per < p.E ? e0 + per : p.E;
+  int pairs = 0, jobs = 0;  // of this lane's experts
+  for (int e = e0; e < e1; ++e) {
+    const int c = static_cast<int>(r.count[e]);
+    pairs += c;
+    jobs += (c + kChunk - 1) / kChunk;
   }
-  if (bad && blockIdx.x == 0) atomicExch(p.status, kInvalidArgStatus);
-  int pairs = 0, jobs = 0;
-  for (int e0 = 0; e0 < p.E; e0 += 32) {
-    const int e = e0 + lane;
-    const int c = e < p.E ? r.cnt[e] : 0, n = (c + kChunk - 1) / kChunk;
-    int sc = c, sn = n;  // inclusive sums over the lanes
+  int sp = pairs, sj = jobs;  // inclusive sums over the lanes
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int a = __shfl_up_sync(0xFFFFFFFFu, sc, d), b = __shfl_up_sync(0xFFFFFFFFu, sn, d);
-      if (lane >= d) sc += a, sn += b;
-    }
-    if (e < p.E) {
-      r.off[e] = static_cast<uint16_t>(pairs + sc - c);
-      r.job[e] = static_cast<uint16_t>(jobs + sn - n);
-      for (int q = 0; q < n; ++q) r.job_e[jobs + sn - n + q] = static_cast<uint16_t>(e);
-      r.cnt[e] = 0;  // counted again below
-    }
-    pairs += __shfl_sync(0xFFFFFFFFu, sc, 31);
-    jobs += __shfl_sync(0xFFFFFFFFu, sn, 31);
+  for (int d = 1; d < 32; d <<= 1) {
+    const int a = __shfl_up_sync(0xFFFFFFFFu, sp, d), b = __shfl_up_sync(0xFFFFFFFFu, sj, d);
+    if (lane >= d) sp += a, sj += b;
+  }
+  const int all = __shfl_sync(0xFFFFFFFFu, sj, 31);
+  int at = sp - pairs, job = sj - jobs;
+  for (int e = e0; e < e1; ++e) {
+    const int c = static_cast<int>(r.count[e]);
+    r.cnt[e] = static_cast<uint16_t>(c);
+    r.off[e] = static_cast<uint16_t>(at);
+    r.job[e] = static_cast<uint16_t>(job);
+    r.next[e] = static_cast<uint16_t>(at);
+    at += c;
+    for (int n = (c + kChunk - 1) / kChunk; n > 0; --n) r.job_e[job++] = static_cast<uint16_t>(e);
   }
   __syncwarp();
   for (int p0 = 0; p0 < P; p0 += 32) {
-    int id = p0 + lane < P ? __ldg(p.ids + p0 + lane) : -1;
-    if (id >= p.E) id = -1;
+    const int id = p0 + lane < P ? r.ids[p0 + lane] : 0xFFFF;
     const uint32_t same = __match_any_sync(0xFFFFFFFFu, id);
     const uint32_t below = same & ((1u << lane) - 1u);
-    const int at = id >= 0 ? r.cnt[id] : 0;
+    const int first = id != 0xFFFF ? r.next[id] : 0;
     __syncwarp();
-    if (id >= 0) {
-      r.list[r.off[id] + at + __popc(below)] = static_cast<uint16_t>(p0 + lane);
-      if (below == 0u) r.cnt[id] = static_cast<uint16_t>(at + __popc(same));
+    if (id != 0xFFFF) {
+      r.list[first + __popc(below)] = static_cast<uint16_t>(p0 + lane);
+      if (below == 0u) r.next[id] = static_cast<uint16_t>(first + __popc(same));
     }
     __syncwarp();
   }
-  return jobs;
+  return all;
 }
 
 // This CTA's run of K-blocks, cut into units: unit u = tile * jobs + job.
@@ -740,6 +749,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   Routing r;
   r.list = reinterpret_cast<uint16_t*>(smem + C::kOffList);
   r.cnt = reinterpret_cast<uint16_t*>(smem + C::kOffCnt);
+  r.count = reinterpret_cast<uint32_t*>(smem + C::kOffCount);
+  r.ids = reinterpret_cast<uint16_t*>(smem + C::kOffIds);
+  r.next = reinterpret_cast<uint16_t*>(smem + C::kOffNext);
   r.off = reinterpret_cast<uint16_t*>(smem + C::kOffOff);
   r.job = reinterpret_cast<uint16_t*>(smem + C::kOffJob);
   r.job_e = reinterpret_cast<uint16_t*>(smem + C::kOffJobE);
@@ -758,6 +770,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   int* jobs_slot = words + 3;
 
   const int warp = static_cast<int>(threadIdx.x) >> 5, lane = threadIdx.x & 31;
+  for (int e = threadIdx.x; e < p.E; e += C::kThreads) r.count[e] = 0u;
   if (threadIdx.x == 0) {
     prefetch_tmap(&tmW);
     for (int s = 0; s < C::STAGES; ++s) {
@@ -778,12 +791,15 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
+  __syncthreads();
   // UP: everything it reads may come from the kernel in front.  DOWN: that is
   // UP, which waited itself; only h is new.
   if (C::PHASE == UP) grid_wait_prerequisites();
   grid_launch_dependents();
+  count_pairs(p, r);
+  __syncthreads();
   if (warp == C::kFillWarp0) {
-    const int jobs = sort_pairs(p, r);
+    const int jobs = place_pairs(p, r);
     if (lane == 0) *jobs_slot = jobs;
   }
   tc_fence_before();
