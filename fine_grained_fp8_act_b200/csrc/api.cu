@@ -1034,6 +1034,7 @@ static NormActArgs norm_act_args(int64_t M, int64_t K, int block, void* xq_e4m3,
   a.K = static_cast<int>(K);
   a.Kb = ceil_div(K, block);
   a.group = block;
+  a.group_shift = block == 128 ? 7 : block == 64 ? 6 : 5;
   a.xq = static_cast<uint8_t*>(xq_e4m3);
   a.xs = x_scale;
   return a;
@@ -1066,11 +1067,12 @@ fg8_status fg8_rmsnorm_quant(const void* x_bf16, int64_t M, int64_t K, int64_t l
   a.ld_x2 = ld_residual;
   a.weight = weight_bf16;
   a.eps = eps;
+  a.inv_k = 1.0f / static_cast<float>(K);
   a.x2_out = residual_out_bf16;
   a.ld_x2_out = ld_residual_out;
   a.y = y_bf16;
   a.ld_y = ld_y;
-  return cuda_status(launch_rmsnorm_quant(a, fmt, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_rmsnorm_quant(a, fmt, dev.sms, static_cast<cudaStream_t>(stream)));
 }
 
 fg8_status fg8_silu_mul_quant(const void* gate_bf16, const void* up_bf16, int64_t M, int64_t K, int64_t ld_gate,

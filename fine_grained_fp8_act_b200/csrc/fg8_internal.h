@@ -55,9 +55,10 @@ struct NormActArgs {
   const void* x2;      // bf16 [M, K], row stride ld_x2: the residual (nullptr: none), or up
   int64_t ld_x2;
   const void* weight;  // rms norm: bf16 [K]
-  float eps;
+  float eps, inv_k;    // inv_k: 1 / K
   int M, K, Kb;
   int group;           // 128, 64 or 32
+  int group_shift;     // log2(group)
   uint8_t* xq;
   void* xs;
   void* x2_out;        // rms norm: bf16(x + residual), row stride ld_x2_out, or nullptr
@@ -65,7 +66,7 @@ struct NormActArgs {
   void* y;             // bf16 of the values that were quantized, row stride ld_y, or nullptr
   int64_t ld_y;
 };
-cudaError_t launch_rmsnorm_quant(const NormActArgs& a, int fmt, cudaStream_t s);
+cudaError_t launch_rmsnorm_quant(const NormActArgs& a, int fmt, int num_sms, cudaStream_t s);
 cudaError_t launch_silu_mul_quant(const NormActArgs& a, int fmt, int num_sms, cudaStream_t s);
 
 // Softmax routing of T tokens over E experts (moe_route.cu).

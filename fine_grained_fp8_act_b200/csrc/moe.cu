@@ -569,7 +569,9 @@ __device__ __forceinline__ void finish_up(const MoeParams& p, const Routing& r, 
     for (int c = et >> 5; c < n; c += C::kEpiThreads / 32) {
       const float4 g = *reinterpret_cast<const float4*>(stage + c * 128 + lane * 4);
       const float4 u = *reinterpret_cast<const float4*>(stage + (C::kStagePairs + c) * 128 + lane * 4);
-      float f[4] = {silu_mul(g.x, u.x), silu_mul(g.y, u.y), silu_mul(g.z, u.z), silu_mul(g.w, u.w)};
+      const float2 f01 = silu_mul2(make_float2(g.x, g.y), make_float2(u.x, u.y));
+      const float2 f23 = silu_mul2(make_float2(g.z, g.w), make_float2(u.z, u.w));
+      float f[4] = {f01.x, f01.y, f23.x, f23.y};
       float amax = 0.0f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {

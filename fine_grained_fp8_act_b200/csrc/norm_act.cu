@@ -8,14 +8,16 @@
 // then, per token and group of 128 (64, 32) channels, the scale and codes of
 // quant_math.cuh.  All of it is float32 and v is never rounded to bf16 on
 // its way to the codes: a bf16 step in between would move a group's amax, and
-// with it every code of the group, by up to 2^-9.  bf16 outputs (the new
+// with it every code of the group, by up to 2^-8.  bf16 outputs (the new
 // residual z, v itself) are rounded once.
 //
-// Both are streams bound by HBM: 16-byte loads and stores, 16 channels per
-// thread and step, everything between in registers.
+// Both are streams bound by HBM.  A lane owns 8 neighbouring channels (16
+// bytes of bf16), so a group is 16, 8 or 4 lanes.
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
+
+#include <atomic>
 
 #include "fg8_internal.h"
 #include "ptx.cuh"
@@ -26,216 +28,530 @@ namespace {
 
 using namespace qm;
 
-__device__ __forceinline__ void load16(const uint16_t* p, float (&f)[16]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p), b = *reinterpret_cast<const uint4*>(p + 8);
-  float lo[8], hi[8];
-  unpack_bf16x8(a, lo);
-  unpack_bf16x8(b, hi);
+__device__ __forceinline__ void unpack8(const uint4& v, float2 (&f)[4]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    f[i] = lo[i];
-    f[8 + i] = hi[i];
+  for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ uint4 pack8(const float2 (&f)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __float22bfloat162_rn(f[i]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ void store16(uint16_t* p, const float (&f)[16]) {
-  uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    w[i] = static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(f[2 * i]))) |
-           (static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(f[2 * i + 1]))) << 16);
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  *reinterpret_cast<uint4*>(p + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+__device__ __forceinline__ uint4 flip_signs(const uint4& v) {  // of 8 packed bf16
+  return make_uint4(v.x ^ 0x80008000u, v.y ^ 0x80008000u, v.z ^ 0x80008000u, v.w ^ 0x80008000u);
 }
 
-// One thread's 16 channels of a group owned by GL neighbouring lanes: the
-// group's amax over the lanes, scale, codes.  Every lane of the warp calls
-// it (lanes without channels pass zeros and `real` false).
-template <int FMT, int GL>
-__device__ __forceinline__ void quantize_group(const NormActArgs& a, const float (&v)[16], int64_t m, int k, int l,
-                                               bool real) {
+__device__ __forceinline__ uint4 ldg16(const void* p, int64_t at) {
+  return *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+}
+
+// A lane's 8 channels k .. k + 7 of token m, as n = -v (quantize_negated):
+// the group's amax over its lanes (a.group / 8 neighbours), scale, codes, and
+// v in bf16 on request.  Every lane of the warp calls it (lanes without
+// channels: zeros, `real` false).
+template <int FMT>
+__device__ __forceinline__ void quantize_lane(const NormActArgs& a, const float2 (&n)[4], int64_t m, int k, bool real) {
   float amax = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[i]));
-#pragma unroll
-  for (int off = GL / 2; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
-  const float s = group_scale(amax);
+  for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(n[i].x), fabsf(n[i].y)));
+  amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+  if (a.group >= 64) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 4));
+  if (a.group >= 128) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 8));
+  const float s = group_scale_fast(amax);
   const uint32_t sbyte = FMT == 1 ? e8m0_ceil_byte(s) : 0u;
-  const uint4 q = quantize16<FMT>(v, s, sbyte);
+  uint32_t q[2];
+  quantize_negated<FMT, 4>(n, s, sbyte, q);
   if (!real) return;
-  *reinterpret_cast<uint4*>(a.xq + m * a.K + k) = q;
-  if (a.y != nullptr) store16(static_cast<uint16_t*>(a.y) + m * a.ld_y + k, v);
-  if (l == 0) {
-    const int64_t g = m * a.Kb + k / (16 * GL);
+  *reinterpret_cast<uint2*>(a.xq + m * a.K + k) = make_uint2(q[0], q[1]);
+  if (a.y != nullptr) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + m * a.ld_y + k) = flip_signs(pack8(n));
+  if ((k & (a.group - 1)) == 0) {
+    const int64_t g = m * a.Kb + (k >> a.group_shift);
     if (FMT == 0) static_cast<float*>(a.xs)[g] = s;
     else static_cast<uint8_t*>(a.xs)[g] = static_cast<uint8_t>(sbyte);
   }
 }
 
-// ------------------------------------------------------------- rms norm ----
-// One CTA of THREADS threads per token; thread t owns channels 16 (t + i
-// THREADS) .. + 15, kept in registers between the sum of squares and the
-// quantization (up to CH steps; longer rows are read twice).
-template <int FMT, int GL, int THREADS, int CH>
-__global__ void __launch_bounds__(THREADS) rmsnorm_quant_kernel(const NormActArgs a) {
+__device__ __forceinline__ float square_sum(const float2 (&z)[4], float ss) {
+  float2 t = make_float2(ss, 0.0f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t = __ffma2_rn(z[i], z[i], t);
+  return t.x + t.y;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+  return v;
+}
+
+// 1 / sqrt(mean + eps): the hardware's approximation (2^-22.9) and one Newton
+// step, y + y/2 (1 - m y y), good to an ulp or so.  m = inf gives NaN in the
+// step, so the approximation's 0 is kept there, and the rows whose squares
+// overflow float32 come out as zeros.
+__device__ __forceinline__ float row_rstd(const NormActArgs& a, float ss) {
+  const float m = fmaf(ss, a.inv_k, a.eps);
+  const float y = rsqrtf(m);
+  const float r = fmaf(0.5f * y, fmaf(-m * y, y, 1.0f), y);
+  return m < __int_as_float(0x7f800000) ? r : y;
+}
+
+// z of a lane's 8 channels, once the row's 1 / rms is known: the new
+// residual, v = z rstd weight, codes.
+template <int FMT>
+__device__ __forceinline__ void finish_norm(const NormActArgs& a, float2 (&z)[4], const uint4& w, float rstd, int64_t m,
+                                            int k, bool real) {
+  if (real && a.x2_out != nullptr)
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.x2_out) + m * a.ld_x2_out + k) = pack8(z);
+  float2 g[4];
+  unpack8(w, g);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) z[i] = __fmul2_rn(__fmul2_rn(z[i], make_float2(-rstd, -rstd)), g[i]);
+  quantize_lane<FMT>(a, z, m, k, real);
+}
+
+// ---------------------------------------------------- rms norm, one row ----
+// Few tokens (or rows past the stream kernel's length): one CTA per token,
+// channels 8 (t + i THREADS) .. + 7 in thread t, plain loads, all of them in
+// flight at once; rows longer than 8 THREADS CH are read twice.
+template <int FMT, int THREADS, int CH>
+__global__ void __launch_bounds__(THREADS) rmsnorm_row_kernel(const NormActArgs a) {
   __shared__ float red[THREADS / 32];
   grid_wait_prerequisites();
   grid_launch_dependents();
-  const int t = threadIdx.x, l = t % GL;
+  const int t = threadIdx.x;
   const int64_t m = blockIdx.x;
-  const uint16_t* x = static_cast<const uint16_t*>(a.x) + m * a.ld_x;
-  const uint16_t* r = a.x2 != nullptr ? static_cast<const uint16_t*>(a.x2) + m * a.ld_x2 : nullptr;
-  const uint16_t* w = static_cast<const uint16_t*>(a.weight);
-  const int steps = (a.K + 16 * THREADS - 1) / (16 * THREADS);
-
-  auto load = [&](int i, float (&z)[16]) {
-    const int k = 16 * (t + i * THREADS);
-    if (k < a.K) {
-      load16(x + k, z);
-      if (r != nullptr) {
-        float f[16];
-        load16(r + k, f);
+  const int steps = (a.K + 8 * THREADS - 1) / (8 * THREADS);
+  auto load = [&](int i, float2 (&z)[4]) {
+    const int k = 8 * (t + i * THREADS);
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (k < a.K) v = ldg16(a.x, m * a.ld_x + k);
+    unpack8(v, z);
+    if (a.x2 != nullptr && k < a.K) {
+      float2 f[4];
+      unpack8(ldg16(a.x2, m * a.ld_x2 + k), f);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) z[j] += f[j];
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) z[j] = 0.0f;
+      for (int j = 0; j < 4; ++j) z[j] = __fadd2_rn(z[j], f[j]);
     }
   };
-
-  float z[CH][16];
+  auto weight = [&](int i) {
+    const int k = 8 * (t + i * THREADS);
+    return k < a.K ? ldg16(a.weight, k) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  float2 z[CH][4];
+  uint4 w[CH];
   float ss = 0.0f;
 #pragma unroll
-  for (int i = 0; i < CH; ++i) load(i, z[i]);
-#pragma unroll
-  for (int i = 0; i < CH; ++i)
-#pragma unroll
-    for (int j = 0; j < 16; ++j) ss = fmaf(z[i][j], z[i][j], ss);
-  for (int i = CH; i < steps; ++i) {
-    float e[16];
-    load(i, e);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) ss = fmaf(e[j], e[j], ss);
+  for (int i = 0; i < CH; ++i) {
+    load(i, z[i]);
+    w[i] = weight(i);
   }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, off);
+  for (int i = 0; i < CH; ++i) ss = square_sum(z[i], ss);
+  for (int i = CH; i < steps; ++i) {
+    float2 e[4];
+    load(i, e);
+    ss = square_sum(e, ss);
+  }
+  ss = warp_sum(ss);
   if (THREADS > 32) {
     if ((t & 31) == 0) red[t >> 5] = ss;
     __syncthreads();
-    ss = 0.0f;
-#pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) ss += red[i];
+    ss = warp_sum((t & 31) < THREADS / 32 ? red[t & 31] : 0.0f);
   }
-  const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, static_cast<float>(a.K)) + a.eps));
-
-  auto finish = [&](int i, float (&e)[16]) {
-    const int k = 16 * (t + i * THREADS);
-    const bool real = k < a.K;
-    if (real) {
-      if (a.x2_out != nullptr) store16(static_cast<uint16_t*>(a.x2_out) + m * a.ld_x2_out + k, e);
-      float g[16];
-      load16(w + k, g);
+  const float rstd = row_rstd(a, ss);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) e[j] = e[j] * rstd * g[j];
-    }
-    quantize_group<FMT, GL>(a, e, m, k, l, real);
-  };
-#pragma unroll
-  for (int i = 0; i < CH; ++i)
-    if (i < steps) finish(i, z[i]);
+  for (int i = 0; i < CH; ++i) {
+    const int k = 8 * (t + i * THREADS);
+    finish_norm<FMT>(a, z[i], w[i], rstd, m, k, k < a.K);
+  }
   for (int i = CH; i < steps; ++i) {
-    float e[16];
+    const int k = 8 * (t + i * THREADS);
+    float2 e[4];
     load(i, e);
-    finish(i, e);
+    finish_norm<FMT>(a, e, weight(i), rstd, m, k, k < a.K);
   }
 }
 
-// ------------------------------------------------------------- silu_mul ----
-// Groups of 16 GL channels, GL neighbouring lanes each; a grid-stride loop
-// over all groups (the group of a lane: (m, kb) = (g / Kb, g % Kb)).
-template <int FMT, int GL>
-__global__ void __launch_bounds__(256) silu_mul_quant_kernel(const NormActArgs a, const int64_t total) {
+// ------------------------------------------------------------ streaming ----
+// Many tokens: one CTA per SM, all warps streaming.  A warp copies what it
+// will read (cp.async, 16 bytes a lane) NBUF items ahead through a ring of
+// its own in shared memory, so that up to 190 KB per SM are in flight without
+// a register spent on them and without a barrier between warps.  An item is S
+// steps of 512 channels; a lane owns 16 neighbouring channels of a step,
+// which halves the per-group work (scale, reciprocal, amax steps) against 8.
+// The copies are made in address order, piece p of 16 bytes by lane p % 32,
+// and stored at piece p ^ (p / 8 % 2): a lane's two pieces, 2 l and 2 l + 1,
+// are then read without bank conflicts.
+constexpr int kStreamSmem = 192 * 1024;
+
+struct LanePieces {
+  int put[2], get[2];  // byte offsets in a step's 1 KB: where this lane's copies go, where its channels are
+  __device__ __forceinline__ explicit LanePieces(int lane) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int p = lane + 32 * h, g = 2 * lane + h;
+      put[h] = (p ^ ((p >> 3) & 1)) * 16;
+      get[h] = (g ^ ((g >> 3) & 1)) * 16;
+    }
+  }
+};
+
+__device__ __forceinline__ void lds_channels(const uint8_t* src, const LanePieces& lp, bool real, float2 (&f)[8]) {
+  uint4 v[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  if (real) {
+    v[0] = *reinterpret_cast<const uint4*>(src + lp.get[0]);
+    v[1] = *reinterpret_cast<const uint4*>(src + lp.get[1]);
+  }
+  float2 lo[4], hi[4];
+  unpack8(v[0], lo);
+  unpack8(v[1], hi);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = lo[i], f[4 + i] = hi[i];
+}
+
+// 16 values to global memory as bf16.
+template <bool FLIP>
+__device__ __forceinline__ void store_channels(uint16_t* p, const float2 (&f)[8]) {
+  const float2 lo[4] = {f[0], f[1], f[2], f[3]}, hi[4] = {f[4], f[5], f[6], f[7]};
+  const uint4 a = pack8(lo), b = pack8(hi);
+  *reinterpret_cast<uint4*>(p) = FLIP ? flip_signs(a) : a;
+  *reinterpret_cast<uint4*>(p + 8) = FLIP ? flip_signs(b) : b;
+}
+
+// quantize_lane for 16 channels (a group is 8, 4 or 2 lanes), with the places
+// of its outputs: xq the lane's codes, xs its group's scale (in elements).
+template <int FMT>
+__device__ __forceinline__ void quantize_channels(const NormActArgs& a, const float2 (&n)[8], uint8_t* xq, int64_t xs,
+                                                  uint16_t* y, bool lead, bool real) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(n[i].x), fabsf(n[i].y)));
+  amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+  if (a.group >= 64) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+  if (a.group >= 128) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 4));
+  const float s = group_scale_fast(amax);
+  const uint32_t sbyte = FMT == 1 ? e8m0_ceil_byte(s) : 0u;
+  uint32_t q[4];
+  quantize_negated<FMT, 8>(n, s, sbyte, q);
+  if (!real) return;
+  *reinterpret_cast<uint4*>(xq) = make_uint4(q[0], q[1], q[2], q[3]);
+  if (a.y != nullptr) store_channels<true>(y, n);
+  if (lead) {
+    if (FMT == 0) static_cast<float*>(a.xs)[xs] = s;
+    else static_cast<uint8_t*>(a.xs)[xs] = static_cast<uint8_t>(sbyte);
+  }
+}
+
+// RMS norm: a team of W warps per token (up to 32 / W tokens at a time),
+// whose weight stays in registers; the team's sum of squares meets in shared
+// memory at the team's own barrier.
+constexpr int rms_warps(int S) { return S == 1 ? 32 : 24; }
+
+template <int FMT, int S, int OPS, int NBUF>
+__global__ void __launch_bounds__(rms_warps(S) * 32, 1) rmsnorm_stream_kernel(const NormActArgs a, const int W) {
+  constexpr int kItem = S * OPS * 1024;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float red[2][rms_warps(S)];
   grid_wait_prerequisites();
   grid_launch_dependents();
-  constexpr int kGpw = 32 / GL;
-  const int lane = threadIdx.x & 31, oct = lane / GL, l = lane % GL;
-  const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
-  for (int64_t base = warp * kGpw; base < total; base += nwarps * kGpw) {
-    const int64_t g = base + oct;
-    const int64_t m = g / a.Kb;
-    const int k = static_cast<int>(g - m * a.Kb) * (16 * GL) + l * 16;
-    const bool real = g < total && k < a.K;
-    float v[16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int teams = static_cast<int>(blockDim.x >> 5) / W, team = warp / W, wt = warp - team * W;
+  const LanePieces lp(lane);
+  uint8_t* mine = ring + warp * NBUF * kItem;
+  const int base = wt * S * 512;  // the warp's channels: S steps of 512
+  const int k0 = base + lane * 16;
+  uint4 w[S][2];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-    if (real) {
-      float u[16];
-      load16(static_cast<const uint16_t*>(a.x) + m * a.ld_x + k, v);
-      load16(static_cast<const uint16_t*>(a.x2) + m * a.ld_x2 + k, u);
+  for (int s = 0; s < S; ++s) {
+    const int k = k0 + s * 512;
+    w[s][0] = k < a.K ? ldg16(a.weight, k) : make_uint4(0u, 0u, 0u, 0u);
+    w[s][1] = k < a.K ? ldg16(a.weight, k + 8) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  // (M < 2^31 and the stride is at most 148 x 32: 32 unsigned bits hold both)
+  const uint32_t stride = gridDim.x * teams, first = blockIdx.x * teams + team, M = a.M;
+  uint32_t mi = first;  // the next token to copy
+  const uint16_t* px = static_cast<const uint16_t*>(a.x) + first * a.ld_x + base + lane * 8;
+  const uint16_t* pr = static_cast<const uint16_t*>(a.x2) + first * a.ld_x2 + base + lane * 8;
+  auto issue = [&](int buf) {
+    if (mi < M) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = silu_mul(v[i], u[i]);
+      for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (base + s * 512 + h * 256 + lane * 8 < a.K) {
+            uint8_t* dst = mine + buf * kItem + s * OPS * 1024 + lp.put[h];
+            cp_async16(dst, px + s * 512 + h * 256);
+            if (OPS == 2) cp_async16(dst + 1024, pr + s * 512 + h * 256);
+          }
+      mi += stride;
+      px += stride * a.ld_x;
+      if (OPS == 2) pr += stride * a.ld_x2;
     }
-    quantize_group<FMT, GL>(a, v, m, k, l, real);
+    cp_async_commit();  // empty past the end: the count of groups stays that of the items
+  };
+#pragma unroll
+  for (int n = 0; n < NBUF - 1; ++n) issue(n);
+  const bool lead = (k0 & (a.group - 1)) == 0;
+  int buf = 0, ahead = NBUF - 1, flip = 0;
+  for (uint32_t m = first; m < M; m += stride) {
+    __syncwarp();  // every lane has read the buffer that is filled now
+    issue(ahead);
+    cp_async_wait_group<NBUF - 1>();
+    __syncwarp();
+    float2 z[S][8];
+    float2 ss = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const uint8_t* src = mine + buf * kItem + s * OPS * 1024;
+      const bool real = k0 + s * 512 < a.K;
+      lds_channels(src, lp, real, z[s]);
+      if (OPS == 2) {
+        float2 f[8];
+        lds_channels(src + 1024, lp, real, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[s][j] = __fadd2_rn(z[s][j], f[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = __ffma2_rn(z[s][j], z[s][j], ss);
+    }
+    float sum = warp_sum(ss.x + ss.y);
+    if (W > 1) {
+      // two sets in turn: a warp ahead by one token writes the other one
+      if (lane == 0) red[flip][warp] = sum;
+      named_barrier_sync(1 + team, W * 32);
+      sum = warp_sum(lane < W ? red[flip][team * W + lane] : 0.0f);
+      flip ^= 1;
+    }
+    const float rstd = row_rstd(a, sum);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const bool real = k0 + s * 512 < a.K;
+      const int k = k0 + s * 512;
+      if (OPS == 2 && real) store_channels<false>(static_cast<uint16_t*>(a.x2_out) + m * a.ld_x2_out + k, z[s]);
+      float2 lo[4], hi[4];
+      unpack8(w[s][0], lo);
+      unpack8(w[s][1], hi);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        z[s][j] = __fmul2_rn(__fmul2_rn(z[s][j], make_float2(-rstd, -rstd)), j < 4 ? lo[j & 3] : hi[j & 3]);
+      quantize_channels<FMT>(a, z[s], a.xq + static_cast<int64_t>(m) * a.K + k,
+                             static_cast<int64_t>(m) * a.Kb + (k >> a.group_shift),
+                             static_cast<uint16_t*>(a.y) + m * a.ld_y + k, lead, real);
+    }
+    buf = buf + 1 == NBUF ? 0 : buf + 1;
+    ahead = ahead + 1 == NBUF ? 0 : ahead + 1;
   }
 }
 
-template <int FMT, int GL>
-cudaError_t launch_rms(const NormActArgs& a, cudaLaunchConfig_t& cfg) {
-  const int n16 = (a.K + 15) / 16;
+// silu(gate) * up: an item is 512 channels of a token (the last of a token
+// may be shorter).
+constexpr int kSiluWarps = 32, kSiluBuffers = 3;
+
+template <int FMT>
+__global__ void __launch_bounds__(kSiluWarps * 32, 1) silu_mul_stream_kernel(const NormActArgs a, const int per_row,
+                                                                             const int64_t items) {
+  constexpr int kItem = 2048, NBUF = kSiluBuffers;
+  static_assert(kSiluWarps * NBUF * kItem <= kStreamSmem, "ring");
+  extern __shared__ __align__(16) uint8_t ring[];
+  grid_wait_prerequisites();
+  grid_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const LanePieces lp(lane);
+  uint8_t* mine = ring + warp * NBUF * kItem;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kSiluWarps;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kSiluWarps + warp;
+  // (token, item of it) of the next copy and of the next result; both step by
+  // stride items, the token's share of which is divided once
+  const int64_t dm = stride / per_row;
+  const int dj = static_cast<int>(stride - dm * per_row);
+  int64_t mi = first / per_row, mo = mi;
+  int ji = static_cast<int>(first - mi * per_row), jo = ji;
+  auto step = [&](int64_t& m, int& j) {
+    m += dm;
+    j += dj;
+    if (j >= per_row) {
+      j -= per_row;
+      ++m;
+    }
+  };
+  auto issue = [&](int buf) {
+    if (mi < a.M) {
+      const int k = ji * 512 + lane * 8;
+      const uint16_t* g = static_cast<const uint16_t*>(a.x) + mi * a.ld_x + k;
+      const uint16_t* u = static_cast<const uint16_t*>(a.x2) + mi * a.ld_x2 + k;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (k + h * 256 < a.K) {
+          uint8_t* dst = mine + buf * kItem + lp.put[h];
+          cp_async16(dst, g + h * 256);
+          cp_async16(dst + 1024, u + h * 256);
+        }
+      step(mi, ji);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int n = 0; n < NBUF - 1; ++n) issue(n);
+  const bool lead = (lane * 16 & (a.group - 1)) == 0;
+  int buf = 0, ahead = NBUF - 1;
+  for (int64_t i = first; i < items; i += stride) {
+    __syncwarp();
+    issue(ahead);
+    cp_async_wait_group<NBUF - 1>();
+    __syncwarp();
+    const int k = jo * 512 + lane * 16;
+    const bool real = k < a.K;
+    const uint8_t* src = mine + buf * kItem;
+    float2 v[8], u[8];
+    lds_channels(src, lp, real, v);
+    lds_channels(src + 1024, lp, real, u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = silu_mul2<true>(v[j], u[j]);
+    quantize_channels<FMT>(a, v, a.xq + mo * a.K + k, mo * a.Kb + (k >> a.group_shift),
+                           static_cast<uint16_t*>(a.y) + mo * a.ld_y + k, lead, real);
+    step(mo, jo);
+    buf = buf + 1 == NBUF ? 0 : buf + 1;
+    ahead = ahead + 1 == NBUF ? 0 : ahead + 1;
+  }
+}
+
+template <int FMT>
+__device__ __forceinline__ void finish_silu(const NormActArgs& a, const uint4& g, const uint4& u, int64_t m, int k,
+                                            bool real) {
+  float2 v[4], f[4];
+  unpack8(g, v);
+  unpack8(u, f);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = silu_mul2<true>(v[j], f[j]);
+  quantize_lane<FMT>(a, v, m, k, real);
+}
+
+// Few tokens: a warp per 256 channels, plain loads.
+template <int FMT>
+__global__ void __launch_bounds__(128) silu_mul_row_kernel(const NormActArgs a, const int per_row, const int64_t items) {
+  grid_wait_prerequisites();
+  grid_launch_dependents();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (i >= items) return;
+  const int64_t m = i / per_row;
+  const int k = static_cast<int>(i - m * per_row) * 256 + (threadIdx.x & 31) * 8;
+  const bool real = k < a.K;
+  uint4 g = make_uint4(0u, 0u, 0u, 0u), u = g;
+  if (real) {
+    g = ldg16(a.x, m * a.ld_x + k);
+    u = ldg16(a.x2, m * a.ld_x2 + k);
+  }
+  finish_silu<FMT>(a, g, u, m, k, real);
+}
+
+// Launch with the stream's dynamic shared memory (opted in once per device).
+template <class... P, class... A>
+cudaError_t launch_stream(void (*kern)(P...), std::atomic<uint64_t>& configured, int warps, cudaLaunchConfig_t& cfg,
+                          A... args) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = 1ull << (dev & 63);
+  if ((configured.load(std::memory_order_acquire) & bit) == 0) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_release);
+  }
+  cfg.blockDim = dim3(static_cast<unsigned>(warps * 32));
+  cfg.dynamicSmemBytes = kStreamSmem;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int FMT, int S, int OPS, int NBUF>
+cudaError_t rms_stream(const NormActArgs& a, int W, int warps, cudaLaunchConfig_t& cfg) {
+  static std::atomic<uint64_t> configured{0};
+  if (warps * NBUF * S * OPS * 1024 > kStreamSmem) return cudaErrorInvalidValue;
+  return launch_stream(rmsnorm_stream_kernel<FMT, S, OPS, NBUF>, configured, warps, cfg, a, W);
+}
+
+template <int FMT>
+cudaError_t launch_rms(const NormActArgs& a, int num_sms, cudaLaunchConfig_t& cfg) {
+  const int n = (a.K + 511) / 512;  // steps of 512 channels in a row
+  const int S = n <= 32 ? 1 : 2, W = (n + S - 1) / S;
+  if (W <= rms_warps(S)) {
+    const int teams = rms_warps(S) / W, warps = teams * W;
+    // A team's ring pays from a few tokens on; below that the one-row kernel
+    // has more loads in flight.  us, stream / row kernel, float scales: with
+    // a residual 600 x 12288 (4 a team) 13 / 12, 1200 x 7168 (4) 15 / 17,
+    // 2400 x 7168 (8) 26 / 41, 1200 x 4096 (2) 10 / 8, but 16384 x 512 (3)
+    // 10 / 18; without 600 x 7168 (2) 6.4 / 8.6, 300 x 7168 (1) 4.8 / 5.5.
+    const int64_t least = a.x2 == nullptr || n == 1 ? 2 : 4;
+    if (static_cast<int64_t>(a.M) >= least * num_sms * teams) {
+      cfg.gridDim = dim3(static_cast<unsigned>(num_sms));
+      if (a.x2 == nullptr)
+        return S == 1 ? rms_stream<FMT, 1, 1, 4>(a, W, warps, cfg) : rms_stream<FMT, 2, 1, 4>(a, W, warps, cfg);
+      if (S == 2) return rms_stream<FMT, 2, 2, 2>(a, W, warps, cfg);
+      return warps <= 24 ? rms_stream<FMT, 1, 2, 4>(a, W, warps, cfg) : rms_stream<FMT, 1, 2, 3>(a, W, warps, cfg);
+    }
+  }
   cfg.gridDim = dim3(static_cast<unsigned>(a.M));
 #define FG8_RMS(T, C) \
-  { cfg.blockDim = dim3(T); return cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<FMT, GL, T, C>, a); }
-  if (n16 <= 32) FG8_RMS(32, 1)
-  if (n16 <= 64) FG8_RMS(64, 1)
-  if (n16 <= 128) FG8_RMS(128, 1)
-  if (n16 <= 256) FG8_RMS(256, 1)
-  if (n16 <= 512) FG8_RMS(256, 2)
-  if (n16 <= 768) FG8_RMS(256, 3)
-  FG8_RMS(512, 3)
+  { cfg.blockDim = dim3(T); return cudaLaunchKernelEx(&cfg, rmsnorm_row_kernel<FMT, T, C>, a); }
+  if (a.K <= 256) FG8_RMS(32, 1)
+  if (a.K <= 512) FG8_RMS(64, 1)
+  if (a.K <= 1024) FG8_RMS(128, 1)
+  if (a.K <= 2048) FG8_RMS(256, 1)
+  if (a.K <= 4096) FG8_RMS(512, 1)
+  if (a.K <= 8192) FG8_RMS(1024, 1)
+  if (a.K <= 12288) FG8_RMS(768, 2)
+  FG8_RMS(1024, 2)
 #undef FG8_RMS
 }
 
-}  // namespace
+template <int FMT>
+cudaError_t launch_silu(const NormActArgs& a, int num_sms, cudaLaunchConfig_t& cfg) {
+  const int per_row = (a.K + 511) / 512;
+  // us, stream / row kernel, float scales: 512 x 14336 (3 items a warp) 10.4 /
+  // 9.2, 1024 x 14336 (6) 16.6 / 16.8, 8192 x 2048 (7) 16.9 / 19.0
+  if (static_cast<int64_t>(a.M) * per_row >= static_cast<int64_t>(6) * num_sms * kSiluWarps) {
+    static std::atomic<uint64_t> configured{0};
+    cfg.gridDim = dim3(static_cast<unsigned>(num_sms));
+    return launch_stream(silu_mul_stream_kernel<FMT>, configured, kSiluWarps, cfg, a, per_row,
+                         static_cast<int64_t>(a.M) * per_row);
+  }
+  const int row = (a.K + 255) / 256;
+  const int64_t items = static_cast<int64_t>(a.M) * row;
+  cfg.gridDim = dim3(static_cast<unsigned>((items + 3) / 4));
+  cfg.blockDim = dim3(128);
+  return cudaLaunchKernelEx(&cfg, silu_mul_row_kernel<FMT>, a, row, items);
+}
 
-cudaError_t launch_rmsnorm_quant(const NormActArgs& a, int fmt, cudaStream_t s) {
+cudaLaunchConfig_t overlapped(cudaLaunchAttribute (&attr)[1], cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaErrorInvalidValue;
-  if (a.group == 128) e = fmt == 0 ? launch_rms<0, 8>(a, cfg) : launch_rms<1, 8>(a, cfg);
-  else if (a.group == 64) e = fmt == 0 ? launch_rms<0, 4>(a, cfg) : launch_rms<1, 4>(a, cfg);
-  else if (a.group == 32) e = fmt == 0 ? launch_rms<0, 2>(a, cfg) : launch_rms<1, 2>(a, cfg);
+  return cfg;
+}
+
+}  // namespace
+
+cudaError_t launch_rmsnorm_quant(const NormActArgs& a, int fmt, int num_sms, cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = overlapped(attr, s);
+  const cudaError_t e = fmt == 0 ? launch_rms<0>(a, num_sms, cfg) : launch_rms<1>(a, num_sms, cfg);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
 cudaError_t launch_silu_mul_quant(const NormActArgs& a, int fmt, int num_sms, cudaStream_t s) {
-  const int64_t total = static_cast<int64_t>(a.M) * a.Kb;
-  const int64_t per_block = 8 * (32 / (a.group / 16));
-  int64_t blocks = (total + per_block - 1) / per_block;
-  const int64_t cap = static_cast<int64_t>(num_sms) * 8;
-  if (blocks > cap) blocks = cap;
-  cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaErrorInvalidValue;
-#define FG8_SM(F, GL) cudaLaunchKernelEx(&cfg, silu_mul_quant_kernel<F, GL>, a, total)
-  if (a.group == 128) e = fmt == 0 ? FG8_SM(0, 8) : FG8_SM(1, 8);
-  else if (a.group == 64) e = fmt == 0 ? FG8_SM(0, 4) : FG8_SM(1, 4);
-  else if (a.group == 32) e = fmt == 0 ? FG8_SM(0, 2) : FG8_SM(1, 2);
-#undef FG8_SM
+  cudaLaunchConfig_t cfg = overlapped(attr, s);
+  const cudaError_t e = fmt == 0 ? launch_silu<0>(a, num_sms, cfg) : launch_silu<1>(a, num_sms, cfg);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

@@ -71,8 +71,75 @@ __device__ __forceinline__ void unpack_bf16x8(const uint4& v, float (&f)[8]) {
   }
 }
 
-// g / (1 + exp(-g)) * u in float32.
-__device__ __forceinline__ float silu_mul(float g, float u) { return __fdiv_rn(g, 1.0f + expf(-g)) * u; }
+__device__ __forceinline__ float ex2_approx(float x) {  // 2^x, relative error 2^-22; below 2^-126: 0
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {  // 1 / x within one ulp (x in [1, 2] here)
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// silu(g) * u for two values, in float32.  With e = exp(-|g|), silu(g) is
+// g / (1 + e) for g >= 0 and g e / (1 + e) below: the denominator lies in
+// [1, 2], so nothing overflows and the approximate reciprocal is good to an
+// ulp.  e = 2^t with t = -|g| log2(e) carried as a float and its remainder,
+// 2^(hi + lo) = 2^hi (1 + lo ln 2): the remainder would cost |g| 2^-25 of e
+// otherwise.  About 11 2^-24 relative in all; |g| e below 88 2^-126 becomes 0.
+// NEG: the negated value.
+template <bool NEG = false>
+__device__ __forceinline__ float2 silu_mul2(float2 g, float2 u) {
+  const float2 a = make_float2(-fabsf(g.x), -fabsf(g.y));
+  constexpr float kL = 1.44269502162933349609375f;  // log2(e), rounded to float32
+  constexpr float kLLo = 1.92596299112661746887e-8f;  // log2(e) - kL
+  constexpr float kLn2 = 0.693147180559945309417f;
+  const float2 L = make_float2(kL, kL), LLo = make_float2(kLLo, kLLo), N = make_float2(kLn2, kLn2);
+  const float2 hi = __fmul2_rn(a, L);
+  const float2 lo = __ffma2_rn(a, LLo, __ffma2_rn(a, L, make_float2(-hi.x, -hi.y)));
+  float2 e = make_float2(ex2_approx(hi.x), ex2_approx(hi.y));
+  e = __ffma2_rn(e, __fmul2_rn(lo, N), e);
+  const float2 d = __fadd2_rn(e, make_float2(1.0f, 1.0f));
+  const float2 n = __fmul2_rn(g, make_float2(g.x < 0.0f ? e.x : 1.0f, g.y < 0.0f ? e.y : 1.0f));
+  const float rx = rcp_approx(d.x), ry = rcp_approx(d.y);
+  return __fmul2_rn(__fmul2_rn(n, NEG ? make_float2(-rx, -ry) : make_float2(rx, ry)), u);
+}
+
+// amax / 448 correctly rounded, as __fdiv_rn would give it (amax below 2^-98
+// ends at the floor either way; above, every step is exact or normal).
+__device__ __forceinline__ float group_scale_fast(float amax) {
+  constexpr float kInv = 1.0f / 448.0f;  // RN(1 / 448)
+  return fmaxf(div_rn_from_rcp(amax, 448.0f, kInv), kMinScale);
+}
+
+// Codes of values v that float32 arithmetic made (not of given bf16 values),
+// which come NEGATED, n = -v.  The quotient takes one FMA correction of
+// q0 = v RN(1/s): q1 = q0 - (q0 s - v) RN(1/s), which is v / s exactly where
+// that is a float32, so ties between two codes are kept, and before its
+// rounding within 2^-23 ulp of it otherwise.  With n in place of v both steps
+// are plain FMAs, and a zero keeps its sign without being given it: for
+// v = -0 the correction is (+0)(-y) + (-0) = -0.
+template <int FMT, int N>
+__device__ __forceinline__ void quantize_negated(const float2 (&n)[N], float s, uint32_t sbyte,
+                                                 uint32_t (&codes)[N / 2]) {
+  float2 q[N];
+  if (FMT == 0) {
+    const float y = -__frcp_rn(s);
+    const float2 Y = make_float2(y, y), S = make_float2(s, s);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 q0 = __fmul2_rn(n[i], Y);
+      q[i] = __ffma2_rn(__ffma2_rn(q0, S, n[i]), Y, q0);
+    }
+  } else {
+    const float inv = -e8m0_reciprocal(sbyte);
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = __fmul2_rn(n[i], make_float2(inv, inv));
+  }
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) codes[i] = pack_e4m3x4(q[2 * i].x, q[2 * i].y, q[2 * i + 1].x, q[2 * i + 1].y);
+}
 
 // Quantize 16 values (two 16-byte bf16 loads) with the group's scale;
 // returns 16 packed e4m3 bytes.

@@ -9,6 +9,7 @@ FP8 量化 ... 完全指南", §一 and §七): weights as torch.float8_e4m3fn, 
 weight_scale_inv per 128x128 block shaped (ceil(out/128), ceil(in/128)),
 float32 or torch.float8_e8m0fnu for scale_fmt "ue8m0".
 """
+import contextlib
 from typing import Optional, Tuple
 
 import torch
@@ -30,7 +31,16 @@ def scale_fmt_code(scale_fmt) -> int:
 
 
 def _stream(t: torch.Tensor) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream
+    # the handle alone: a Stream object costs as much as a small kernel's launch
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device: torch.device):
+    """torch.cuda.device(device), and nothing where that is the current device already."""
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _cdiv(a: int, b: int) -> int:
@@ -63,6 +73,8 @@ def _check_cuda(t: torch.Tensor, name: str):
 def _check_tensor(t, name: str, shape, dtypes, device):
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
+    if t.shape == shape and t.dtype in dtypes and t.device == device and t.is_contiguous():
+        return
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype not in dtypes:
@@ -105,7 +117,7 @@ def quantize_weight(w: torch.Tensor, scale_fmt="float", block: int = 128) -> Tup
     N, K = w.shape
     wq = torch.empty((N, K), dtype=torch.float8_e4m3fn, device=w.device)
     ws = torch.empty((_cdiv(N, block), _cdiv(K, block)), dtype=_SCALE_DTYPES[fmt], device=w.device)
-    with torch.cuda.device(w.device):
+    with _on(w.device):
         C.fg8_quantize_weight_block(w.data_ptr(), N, K, w.stride(0), wq.data_ptr(), ws.data_ptr(), fmt, block,
                                     _stream(w))
     return wq, ws
@@ -119,7 +131,7 @@ def quantize_act(x: torch.Tensor, scale_fmt="float", block: int = 128) -> Tuple[
     M, K = x.shape
     xq = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
     xs = torch.empty((M, _cdiv(K, block)), dtype=_SCALE_DTYPES[fmt], device=x.device)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         C.fg8_quantize_act_block(x.data_ptr(), M, K, x.stride(0), xq.data_ptr(), xs.data_ptr(), fmt, block,
                                  _stream(x))
     return xq, xs
@@ -135,7 +147,7 @@ def quantize_act_static(x: torch.Tensor, act_scale: torch.Tensor) -> Tuple[torch
     M, K = x.shape
     xq = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
     xs = torch.empty((M, _cdiv(K, 128)), dtype=torch.float32, device=x.device)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         C.fg8_quantize_act_static(x.data_ptr(), M, K, x.stride(0), act_scale.data_ptr(), xq.data_ptr(), xs.data_ptr(),
                                   _stream(x))
     return xq, xs
@@ -170,7 +182,7 @@ def linear(x: torch.Tensor, wq: torch.Tensor, w_scale_inv: torch.Tensor, bias: O
     _check_cuda(x, "x")
     nbytes = C.fg8_linear_block_workspace_bytes(M, N, K, fmt, block)  # 0: the call below reports why
     ws = _workspace(nbytes, x.device, workspace)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         C.fg8_linear_block(x.data_ptr(), M, N, K, x.stride(0), wq.data_ptr(), w_scale_inv.data_ptr(), bp,
                            y.data_ptr(), y.stride(0), fmt, block, ws.data_ptr(), ws.numel() * ws.element_size(),
                            _stream(x))
@@ -197,7 +209,7 @@ def grouped_linear(x: torch.Tensor, row_expert: torch.Tensor, wq: torch.Tensor, 
     y = _output(out, M, N, x.device)
     _check_cuda(x, "x")
     ws = _workspace(C.fg8_grouped_linear_workspace_bytes(M, E, N, K, fmt), x.device, workspace)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         C.fg8_grouped_linear(x.data_ptr(), M, K, x.stride(0), row_expert.data_ptr(), E, N, wq.data_ptr(),
                              w_scale_inv.data_ptr(), bp, y.data_ptr(), y.stride(0), fmt, ws.data_ptr(),
                              ws.numel() * ws.element_size(), _stream(x))
@@ -220,7 +232,7 @@ def linear_static(x: torch.Tensor, act_scale: torch.Tensor, wq: torch.Tensor, w_
     y = _output(out, M, N, x.device)
     _check_cuda(x, "x")
     ws = _workspace(C.fg8_linear_workspace_bytes(M, N, K, C.FG8_SCALE_FLOAT), x.device, workspace)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         C.fg8_linear_static(x.data_ptr(), M, N, K, x.stride(0), act_scale.data_ptr(), wq.data_ptr(),
                             w_scale_inv.data_ptr(), bp, y.data_ptr(), y.stride(0), ws.data_ptr(),
                             ws.numel() * ws.element_size(), _stream(x))
@@ -244,7 +256,7 @@ def gemm_prequant(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_s
     _check_cuda(xq, "xq")
     nbytes = C.fg8_gemm_workspace_bytes(M, N, K, fmt)
     ws = _workspace(nbytes, xq.device, workspace)
-    with torch.cuda.device(xq.device):
+    with _on(xq.device):
         C.fg8_gemm_prequant(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale_inv.data_ptr(), bp,
                             y.data_ptr(), M, N, K, y.stride(0), fmt, ws.data_ptr(), ws.numel() * ws.element_size(),
                             _stream(xq))
@@ -284,7 +296,7 @@ def linear_chain(x: torch.Tensor, layers, scale_fmt="float", workspaces=None):
            for (n, kk), w in zip(dims, workspaces)]
     ys = [torch.empty((M, n), dtype=torch.bfloat16, device=x.device) for n, _ in dims]
     s = _stream(x)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         n0, k0 = dims[0]
         C.fg8_linear_prepare(x.data_ptr(), M, n0, k0, x.stride(0), layers[0][1].data_ptr(), fmt, wss[0].data_ptr(),
                              wss[0].numel(), s)
@@ -310,7 +322,7 @@ def dequantize_weight(wq: torch.Tensor, w_scale_inv: torch.Tensor, scale_fmt="fl
     _check_weight(wq, w_scale_inv, (), N, K, fmt, 128, wq.device)
     _check_cuda(wq, "wq")
     w = torch.empty((N, K), dtype=torch.bfloat16, device=wq.device)
-    with torch.cuda.device(wq.device):
+    with _on(wq.device):
         C.fg8_dequantize_weight(wq.data_ptr(), N, K, w_scale_inv.data_ptr(), fmt, w.data_ptr(), K, _stream(wq))
     return w
 
@@ -323,16 +335,18 @@ def scale_to_ue8m0(scale: torch.Tensor) -> Tuple[torch.Tensor, int]:
         raise ValueError("scale must be a float32 CUDA tensor")
     out = torch.empty(s.shape, dtype=torch.uint8, device=s.device)
     bad = torch.zeros(1, dtype=torch.int32, device=s.device)
-    with torch.cuda.device(s.device):
+    with _on(s.device):
         C.fg8_scale_to_ue8m0(s.data_ptr(), s.numel(), out.data_ptr(), bad.data_ptr(), _stream(s))
     return out.view(torch.float8_e8m0fnu), int(bad.item())
 
 
-def _quantized_outputs(M: int, K: int, fmt: int, block: int, device):
+def _quantized_outputs(x: torch.Tensor, fmt: int, block: int):
+    """e4m3 [M, K] and the scales' [M, ceil(K/block)] for bf16 rows x (rows apart or not: new tensors are contiguous)."""
     if block not in (128, 64, 32):
         raise ValueError(f"block must be 128, 64 or 32, got {block!r}")
-    return (torch.empty((M, K), dtype=torch.float8_e4m3fn, device=device),
-            torch.empty((M, _cdiv(K, block)), dtype=_SCALE_DTYPES[fmt], device=device))
+    M, K = x.shape
+    return (torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format),
+            x.new_empty((M, _cdiv(K, block)), dtype=_SCALE_DTYPES[fmt]))
 
 
 def _check_like(t, name: str, x: torch.Tensor):
@@ -362,11 +376,11 @@ def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, resi
             raise ValueError("residual_out needs a residual")
         _check_like(residual_out, "residual_out", x)
     _check_cuda(x, "x")
-    xq, xs = _quantized_outputs(M, K, fmt, block, x.device)
+    xq, xs = _quantized_outputs(x, fmt, block)
     if residual is not None and residual_out is None:
-        residual_out = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
-    y = torch.empty((M, K), dtype=torch.bfloat16, device=x.device) if return_y else None
-    with torch.cuda.device(x.device):
+        residual_out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    y = torch.empty_like(x, memory_format=torch.contiguous_format) if return_y else None
+    with _on(x.device):
         C.fg8_rmsnorm_quant(x.data_ptr(), M, K, x.stride(0), 0 if residual is None else residual.data_ptr(),
                             K if residual is None else residual.stride(0), weight.data_ptr(), eps, xq.data_ptr(),
                             xs.data_ptr(), fmt, block, 0 if residual_out is None else residual_out.data_ptr(),
@@ -385,9 +399,9 @@ def silu_mul_quant(gate: torch.Tensor, up: torch.Tensor, scale_fmt="float", bloc
     _check_like(up, "up", gate)
     _check_cuda(gate, "gate")
     M, K = gate.shape
-    xq, xs = _quantized_outputs(M, K, fmt, block, gate.device)
-    y = torch.empty((M, K), dtype=torch.bfloat16, device=gate.device) if return_y else None
-    with torch.cuda.device(gate.device):
+    xq, xs = _quantized_outputs(gate, fmt, block)
+    y = torch.empty_like(gate, memory_format=torch.contiguous_format) if return_y else None
+    with _on(gate.device):
         C.fg8_silu_mul_quant(gate.data_ptr(), up.data_ptr(), M, K, gate.stride(0), up.stride(0), xq.data_ptr(),
                              xs.data_ptr(), fmt, block, 0 if y is None else y.data_ptr(), K, _stream(gate))
     return xq, xs, y
@@ -409,9 +423,9 @@ def moe_route(logits: torch.Tensor, k: int, renormalize: bool = True,
     if not 1 <= k <= min(E, 32):
         raise ValueError(f"k must be between 1 and min({E}, 32), got {k}")
     _check_cuda(logits, "logits")
-    ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-    with torch.cuda.device(logits.device):
+    ids = logits.new_empty((T, k), dtype=torch.int32)
+    weights = logits.new_empty((T, k), dtype=torch.float32)
+    with _on(logits.device):
         C.fg8_moe_route(logits.data_ptr(), 1 if logits.dtype == torch.bfloat16 else 0, T, E, logits.stride(0), k,
                         1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), _stream(logits))
     return ids, weights
@@ -451,7 +465,7 @@ def moe_mlp(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: torc
     _check_cuda(x, "x")
     nbytes = C.fg8_moe_mlp_workspace_bytes(T, k, E, H, I, fmt)  # 0: the call below reports why
     ws = _workspace(nbytes, x.device, workspace)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         C.fg8_moe_mlp(x.data_ptr(), 0 if x_scale is None else x_scale.data_ptr(), T, H, x.stride(0), ids.data_ptr(),
                       weights.data_ptr(), k, E, I, w13.data_ptr(), w13_scale_inv.data_ptr(), w2.data_ptr(),
                       w2_scale_inv.data_ptr(), y.data_ptr(), y.stride(0), fmt, ws.data_ptr(),

@@ -64,11 +64,13 @@ def rmsnorm(x, weight, eps, residual):
 
 
 def silu_mul(g, u):
-    """(v, |error|): expf is off by at most 2 ulp (4 U), which 1 + exp(-g) passes on at most whole, then its own
-    sum, the quotient and the product round once each; an exponential past float32's range gives 0."""
+    """(v, |error|) of g e / (1 + e) or g / (1 + e) with e = exp(-|g|) by an exponential that is off by at most 2^-22
+    (4 U): 4 U and 1 U for e, which the quotient passes on at most whole, then the numerator, the denominator, its
+    reciprocal (an ulp, 2 U), the quotient and the product with u: 11 U.  Where e is below float32's normal range,
+    |g| > 126 ln 2 = 87.336, it may be 0: silu is then below 87.4 2^-126 < 1.03e-36 in size, and all of it is lost."""
     g, u = g.to(F64), u.to(F64)
     v = g / (1.0 + torch.exp(-g)) * u
-    return v, v.abs() * (U * 10) + (g < -88.0) * u.abs() * 1e-36
+    return v, v.abs() * (U * 11) + (g < -87.336) * u.abs() * 1.03e-36
 
 
 def quantize_values(v, fmt, block=128):
