@@ -61,6 +61,9 @@ SIGNATURES = {
     "fg8_rmsnorm_quant": (_INT, [_VP, _I64, _I64, _I64, _VP, _I64, _VP, ctypes.c_float, _VP, _VP, _INT, _INT, _VP,
                                  _I64, _VP, _I64, _VP]),
     "fg8_silu_mul_quant": (_INT, [_VP, _VP, _I64, _I64, _I64, _I64, _VP, _VP, _INT, _INT, _VP, _I64, _VP]),
+    "fg8_linear_prepare_rmsnorm": (_INT, [_VP, _I64, _I64, _I64, _I64, _VP, _I64, _VP, ctypes.c_float, _VP, _I64, _VP,
+                                          _I64, _VP, _INT, _VP, _SZ, _VP]),
+    "fg8_linear_prepare_silu_mul": (_INT, [_VP, _VP, _I64, _I64, _I64, _I64, _I64, _VP, _INT, _VP, _SZ, _VP]),
     "fg8_moe_route": (_INT, [_VP, _INT, _I64, _I64, _I64, _I64, _INT, ctypes.c_float, _VP, _VP, _VP]),
     "fg8_moe_mlp_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64, _INT]),
     "fg8_moe_mlp": (_INT, [_VP, _VP, _I64, _I64, _I64, _VP, _VP, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _I64,
@@ -269,6 +272,19 @@ def fg8_rmsnorm_quant(x_bf16, M, K, ld_x, residual_bf16, ld_residual, weight_bf1
 def fg8_silu_mul_quant(gate_bf16, up_bf16, M, K, ld_gate, ld_up, xq_e4m3, x_scale, fmt, block, y_bf16, ld_y, stream):
     _check("fg8_silu_mul_quant", lib().fg8_silu_mul_quant(gate_bf16, up_bf16, M, K, ld_gate, ld_up, xq_e4m3, x_scale,
                                                           fmt, block, y_bf16, ld_y, stream))
+
+
+def fg8_linear_prepare_rmsnorm(x_bf16, M, N, K, ld_x, residual_bf16, ld_residual, weight_bf16, eps, residual_out_bf16,
+                               ld_residual_out, y_bf16, ld_y, w_scale_inv, fmt, workspace, workspace_bytes, stream):
+    _check("fg8_linear_prepare_rmsnorm", lib().fg8_linear_prepare_rmsnorm(
+        x_bf16, M, N, K, ld_x, residual_bf16, ld_residual, weight_bf16, eps, residual_out_bf16, ld_residual_out, y_bf16,
+        ld_y, w_scale_inv, fmt, workspace, workspace_bytes, stream))
+
+
+def fg8_linear_prepare_silu_mul(gate_bf16, up_bf16, M, N, K, ld_gate, ld_up, w_scale_inv, fmt, workspace,
+                                workspace_bytes, stream):
+    _check("fg8_linear_prepare_silu_mul", lib().fg8_linear_prepare_silu_mul(
+        gate_bf16, up_bf16, M, N, K, ld_gate, ld_up, w_scale_inv, fmt, workspace, workspace_bytes, stream))
 
 
 def fg8_moe_route(logits, logits_bf16, T, E, ld_logits, k, renormalize, scale, ids, weights, stream):

@@ -1025,79 +1025,179 @@ fg8_status fg8_scale_to_ue8m0(const void* scale_f32, int64_t n, void* scale_e8m0
 }
 
 // ---- around the linears: norm, activation, routing, few-token experts ----
-// The fields both fused quantizers share; the checks of one bf16 operand.
 static bool rows_ok(const void* p, int64_t ld) { return ld % 8 == 0 && aligned16(p); }
 
-static NormActArgs norm_act_args(int64_t M, int64_t K, int block, void* xq_e4m3, void* x_scale) {
+// Operand checks of the norm and of silu_mul, shared by the forms that write
+// row-major scales and those that prepare a linear's workspace.  FG8_OK for
+// M == 0, like the callers.
+static fg8_status check_rmsnorm(const void* x, int64_t M, int64_t K, int64_t ld_x, const void* r, int64_t ld_r,
+                                const void* w, float eps, const void* ro, int64_t ld_ro, const void* y, int64_t ld_y) {
+  if (M < 0 || K <= 0 || M > kMaxDim || K > kMaxNormWidth || ld_x < K || !(eps > 0.0f) || eps > 3.0e38f)
+    return FG8_ERR_INVALID_ARG;
+  if ((r != nullptr && ld_r < K) || (ro != nullptr && ld_ro < K) || (y != nullptr && ld_y < K) ||
+      (r == nullptr) != (ro == nullptr))
+    return FG8_ERR_INVALID_ARG;
+  if (M == 0) return FG8_OK;
+  if (x == nullptr || w == nullptr) return FG8_ERR_INVALID_ARG;
+  if (K % 16 != 0 || !rows_ok(x, ld_x) || !aligned16(w) || (r != nullptr && (!rows_ok(r, ld_r) || !rows_ok(ro, ld_ro))) ||
+      (y != nullptr && !rows_ok(y, ld_y)))
+    return FG8_ERR_ALIGNMENT;
+  return FG8_OK;
+}
+
+static fg8_status check_silu_mul(const void* g, const void* u, int64_t M, int64_t K, int64_t ld_g, int64_t ld_u,
+                                 const void* y, int64_t ld_y) {
+  if (M < 0 || K <= 0 || M > kMaxDim || K > kMaxNormWidth || ld_g < K || ld_u < K || (y != nullptr && ld_y < K))
+    return FG8_ERR_INVALID_ARG;
+  if (M == 0) return FG8_OK;
+  if (g == nullptr || u == nullptr) return FG8_ERR_INVALID_ARG;
+  if (K % 16 != 0 || !rows_ok(g, ld_g) || !rows_ok(u, ld_u) || (y != nullptr && !rows_ok(y, ld_y)))
+    return FG8_ERR_ALIGNMENT;
+  return FG8_OK;
+}
+
+// Row-major outputs of the stand-alone forms.
+static fg8_status check_codes_out(const void* xq, const void* xs, int fmt) {
+  if (xq == nullptr || xs == nullptr) return FG8_ERR_INVALID_ARG;
+  if (!aligned16(xq) || (fmt == FG8_SCALE_FLOAT && (reinterpret_cast<uintptr_t>(xs) & 3u) != 0))
+    return FG8_ERR_ALIGNMENT;
+  return FG8_OK;
+}
+
+static NormActArgs norm_act_args(int64_t M, int64_t K, int block, void* xq, void* xs) {
   NormActArgs a{};
   a.M = static_cast<int>(M);
   a.K = static_cast<int>(K);
   a.Kb = ceil_div(K, block);
   a.group = block;
   a.group_shift = block == 128 ? 7 : block == 64 ? 6 : 5;
-  a.xq = static_cast<uint8_t*>(xq_e4m3);
-  a.xs = x_scale;
+  a.xq = static_cast<uint8_t*>(xq);
+  a.xs = xs;
+  a.layout = kScaleRowMajor;
   return a;
+}
+
+// Outputs in fg8_linear's workspace, where fg8_linear_run reads them.
+static NormActArgs prepare_norm_act_args(int64_t M, int64_t N, int64_t K, int fmt, void* workspace) {
+  const LinearWs L = linear_ws_layout(M, N, K, fmt);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  NormActArgs a = norm_act_args(M, K, 128, ws + L.xq_off, ws + L.xs_off);
+  a.layout = fmt == FG8_SCALE_FLOAT ? kScaleKMajor : kScaleSfTiles;
+  a.ld_s = L.ld_s;
+  a.Kq = ceil_div(a.Kb, 4);
+  a.M_pad = ceil_div(M, 128) * 128;
+  return a;
+}
+
+// The weight's half of a prepare step, and the checks both forms make of it.
+static fg8_status prepare_weight_scales(int64_t M, int64_t N, int64_t K, const void* w_scale_inv, int fmt,
+                                        void* workspace, cudaStream_t s) {
+  if (fmt != FG8_SCALE_UE8M0) return FG8_OK;
+  return cuda_status(launch_sf_pack(static_cast<const uint8_t*>(w_scale_inv), static_cast<int>(N), sfb_rows(N), 128,
+                                    ceil_div(K, kGroup), 1,
+                                    static_cast<uint8_t*>(workspace) + linear_ws_layout(M, N, K, fmt).wsc_off, s));
+}
+
+static void set_rmsnorm(NormActArgs& a, const void* x, int64_t ld_x, const void* r, int64_t ld_r, const void* w,
+                        float eps, void* ro, int64_t ld_ro, void* y, int64_t ld_y) {
+  a.x = x;
+  a.ld_x = ld_x;
+  a.x2 = r;
+  a.ld_x2 = ld_r;
+  a.weight = w;
+  a.eps = eps;
+  a.inv_k = 1.0f / static_cast<float>(a.K);
+  a.x2_out = ro;
+  a.ld_x2_out = ld_ro;
+  a.y = y;
+  a.ld_y = ld_y;
+}
+
+static void set_silu_mul(NormActArgs& a, const void* g, int64_t ld_g, const void* u, int64_t ld_u, void* y,
+                         int64_t ld_y) {
+  a.x = g;
+  a.ld_x = ld_g;
+  a.x2 = u;
+  a.ld_x2 = ld_u;
+  a.y = y;
+  a.ld_y = ld_y;
 }
 
 fg8_status fg8_rmsnorm_quant(const void* x_bf16, int64_t M, int64_t K, int64_t ld_x, const void* residual_bf16,
                              int64_t ld_residual, const void* weight_bf16, float eps, void* xq_e4m3, void* x_scale,
                              fg8_scale_fmt fmt, int block, void* residual_out_bf16, int64_t ld_residual_out,
                              void* y_bf16, int64_t ld_y, void* stream) {
-  if (!fmt_ok(fmt) || (block != 128 && !small_block(block)) || M < 0 || K <= 0 || M > kMaxDim || K > kMaxNormWidth ||
-      ld_x < K || !(eps > 0.0f) || eps > 3.0e38f)
-    return FG8_ERR_INVALID_ARG;
-  if ((residual_bf16 != nullptr && ld_residual < K) || (residual_out_bf16 != nullptr && ld_residual_out < K) ||
-      (y_bf16 != nullptr && ld_y < K) || (residual_bf16 == nullptr) != (residual_out_bf16 == nullptr))
-    return FG8_ERR_INVALID_ARG;
+  if (!fmt_ok(fmt) || (block != 128 && !small_block(block))) return FG8_ERR_INVALID_ARG;
+  if (fg8_status st = check_rmsnorm(x_bf16, M, K, ld_x, residual_bf16, ld_residual, weight_bf16, eps,
+                                    residual_out_bf16, ld_residual_out, y_bf16, ld_y);
+      st != FG8_OK)
+    return st;
   if (M == 0) return FG8_OK;
-  if (x_bf16 == nullptr || weight_bf16 == nullptr || xq_e4m3 == nullptr || x_scale == nullptr)
-    return FG8_ERR_INVALID_ARG;
-  if (K % 16 != 0 || !rows_ok(x_bf16, ld_x) || !aligned16(weight_bf16) || !aligned16(xq_e4m3) ||
-      (fmt == FG8_SCALE_FLOAT && (reinterpret_cast<uintptr_t>(x_scale) & 3u) != 0) ||
-      (residual_bf16 != nullptr && (!rows_ok(residual_bf16, ld_residual) || !rows_ok(residual_out_bf16, ld_residual_out))) ||
-      (y_bf16 != nullptr && !rows_ok(y_bf16, ld_y)))
-    return FG8_ERR_ALIGNMENT;
+  if (fg8_status st = check_codes_out(xq_e4m3, x_scale, fmt); st != FG8_OK) return st;
   DeviceInfo dev;
   if (fg8_status st = current_device(&dev); st != FG8_OK) return st;
   NormActArgs a = norm_act_args(M, K, block, xq_e4m3, x_scale);
-  a.x = x_bf16;
-  a.ld_x = ld_x;
-  a.x2 = residual_bf16;
-  a.ld_x2 = ld_residual;
-  a.weight = weight_bf16;
-  a.eps = eps;
-  a.inv_k = 1.0f / static_cast<float>(K);
-  a.x2_out = residual_out_bf16;
-  a.ld_x2_out = ld_residual_out;
-  a.y = y_bf16;
-  a.ld_y = ld_y;
+  set_rmsnorm(a, x_bf16, ld_x, residual_bf16, ld_residual, weight_bf16, eps, residual_out_bf16, ld_residual_out,
+              y_bf16, ld_y);
   return cuda_status(launch_rmsnorm_quant(a, fmt, dev.sms, static_cast<cudaStream_t>(stream)));
 }
 
 fg8_status fg8_silu_mul_quant(const void* gate_bf16, const void* up_bf16, int64_t M, int64_t K, int64_t ld_gate,
                               int64_t ld_up, void* xq_e4m3, void* x_scale, fg8_scale_fmt fmt, int block,
                               void* y_bf16, int64_t ld_y, void* stream) {
-  if (!fmt_ok(fmt) || (block != 128 && !small_block(block)) || M < 0 || K <= 0 || M > kMaxDim || K > kMaxNormWidth ||
-      ld_gate < K || ld_up < K || (y_bf16 != nullptr && ld_y < K))
-    return FG8_ERR_INVALID_ARG;
+  if (!fmt_ok(fmt) || (block != 128 && !small_block(block))) return FG8_ERR_INVALID_ARG;
+  if (fg8_status st = check_silu_mul(gate_bf16, up_bf16, M, K, ld_gate, ld_up, y_bf16, ld_y); st != FG8_OK) return st;
   if (M == 0) return FG8_OK;
-  if (gate_bf16 == nullptr || up_bf16 == nullptr || xq_e4m3 == nullptr || x_scale == nullptr)
-    return FG8_ERR_INVALID_ARG;
-  if (K % 16 != 0 || !rows_ok(gate_bf16, ld_gate) || !rows_ok(up_bf16, ld_up) || !aligned16(xq_e4m3) ||
-      (fmt == FG8_SCALE_FLOAT && (reinterpret_cast<uintptr_t>(x_scale) & 3u) != 0) ||
-      (y_bf16 != nullptr && !rows_ok(y_bf16, ld_y)))
-    return FG8_ERR_ALIGNMENT;
+  if (fg8_status st = check_codes_out(xq_e4m3, x_scale, fmt); st != FG8_OK) return st;
   DeviceInfo dev;
   if (fg8_status st = current_device(&dev); st != FG8_OK) return st;
   NormActArgs a = norm_act_args(M, K, block, xq_e4m3, x_scale);
-  a.x = gate_bf16;
-  a.ld_x = ld_gate;
-  a.x2 = up_bf16;
-  a.ld_x2 = ld_up;
-  a.y = y_bf16;
-  a.ld_y = ld_y;
+  set_silu_mul(a, gate_bf16, ld_gate, up_bf16, ld_up, y_bf16, ld_y);
   return cuda_status(launch_silu_mul_quant(a, fmt, dev.sms, static_cast<cudaStream_t>(stream)));
+}
+
+fg8_status fg8_linear_prepare_rmsnorm(const void* x_bf16, int64_t M, int64_t N, int64_t K, int64_t ld_x,
+                                      const void* residual_bf16, int64_t ld_residual, const void* weight_bf16,
+                                      float eps, void* residual_out_bf16, int64_t ld_residual_out, void* y_bf16,
+                                      int64_t ld_y, const void* w_scale_inv, fg8_scale_fmt fmt, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+  if (fg8_status st = check_gemm_shape(M, N, K, fmt); st != FG8_OK) return st;
+  if (M > kMaxDim - 127) return FG8_ERR_INVALID_ARG;  // rows are padded to 128
+  if (fg8_status st = check_rmsnorm(x_bf16, M, K, ld_x, residual_bf16, ld_residual, weight_bf16, eps,
+                                    residual_out_bf16, ld_residual_out, y_bf16, ld_y);
+      st != FG8_OK)
+    return st;
+  if (M == 0) return FG8_OK;
+  if (w_scale_inv == nullptr) return FG8_ERR_INVALID_ARG;
+  if (fg8_status st = check_workspace(workspace, workspace_bytes, linear_ws_layout(M, N, K, fmt).total); st != FG8_OK)
+    return st;
+  DeviceInfo dev;
+  if (fg8_status st = current_device(&dev); st != FG8_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  NormActArgs a = prepare_norm_act_args(M, N, K, fmt, workspace);
+  set_rmsnorm(a, x_bf16, ld_x, residual_bf16, ld_residual, weight_bf16, eps, residual_out_bf16, ld_residual_out,
+              y_bf16, ld_y);
+  if (fg8_status st = cuda_status(launch_rmsnorm_quant(a, fmt, dev.sms, s)); st != FG8_OK) return st;
+  return prepare_weight_scales(M, N, K, w_scale_inv, fmt, workspace, s);
+}
+
+fg8_status fg8_linear_prepare_silu_mul(const void* gate_bf16, const void* up_bf16, int64_t M, int64_t N, int64_t K,
+                                       int64_t ld_gate, int64_t ld_up, const void* w_scale_inv, fg8_scale_fmt fmt,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  if (fg8_status st = check_gemm_shape(M, N, K, fmt); st != FG8_OK) return st;
+  if (M > kMaxDim - 127) return FG8_ERR_INVALID_ARG;  // rows are padded to 128
+  if (fg8_status st = check_silu_mul(gate_bf16, up_bf16, M, K, ld_gate, ld_up, nullptr, 0); st != FG8_OK) return st;
+  if (M == 0) return FG8_OK;
+  if (w_scale_inv == nullptr) return FG8_ERR_INVALID_ARG;
+  if (fg8_status st = check_workspace(workspace, workspace_bytes, linear_ws_layout(M, N, K, fmt).total); st != FG8_OK)
+    return st;
+  DeviceInfo dev;
+  if (fg8_status st = current_device(&dev); st != FG8_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  NormActArgs a = prepare_norm_act_args(M, N, K, fmt, workspace);
+  set_silu_mul(a, gate_bf16, ld_gate, up_bf16, ld_up, nullptr, 0);
+  if (fg8_status st = cuda_status(launch_silu_mul_quant(a, fmt, dev.sms, s)); st != FG8_OK) return st;
+  return prepare_weight_scales(M, N, K, w_scale_inv, fmt, workspace, s);
 }
 
 fg8_status fg8_moe_route(const void* logits, int logits_bf16, int64_t T, int64_t E, int64_t ld_logits, int64_t k,

@@ -48,7 +48,7 @@ struct ActQuantArgs {
 cudaError_t launch_act_quant(const ActQuantArgs& a, int fmt, int num_sms, cudaStream_t s);
 
 // RMS norm or silu(gate) * up, quantized as an activation (norm_act.cu):
-// codes [M, K] (row stride K) and row-major scales [M, ceil(K / group)].
+// codes [M, K] (row stride K) and scales in `layout`.
 struct NormActArgs {
   const void* x;       // bf16 [M, K], row stride ld_x: x, or the gate
   int64_t ld_x;
@@ -61,6 +61,9 @@ struct NormActArgs {
   int group_shift;     // log2(group)
   uint8_t* xq;
   void* xs;
+  int layout;          // ScaleLayout; K-major (float) and scale-factor tiles (UE8M0) with group 128 only
+  int64_t ld_s;        // kScaleKMajor: column stride
+  int Kq, M_pad;       // kScaleSfTiles, as ActQuantArgs
   void* x2_out;        // rms norm: bf16(x + residual), row stride ld_x2_out, or nullptr
   int64_t ld_x2_out;
   void* y;             // bf16 of the values that were quantized, row stride ld_y, or nullptr

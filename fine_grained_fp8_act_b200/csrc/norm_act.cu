@@ -52,6 +52,31 @@ __device__ __forceinline__ uint4 ldg16(const void* p, int64_t at) {
   return *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
 }
 
+// The scale of token m's group g: row-major, or where the GEMM reads it, which
+// then needs no pass of its own over the scales.  In a scale-factor tile the
+// slots past the last group are set to 2^0 together with it.
+// ROW: known to be row-major (the stream kernels have no register to spare).
+template <int FMT, bool ROW>
+__device__ __forceinline__ void store_scale(const NormActArgs& a, int64_t m, int g, float s, uint32_t sbyte) {
+  if (ROW || a.layout == kScaleRowMajor) {
+    if (FMT == 0) static_cast<float*>(a.xs)[m * a.Kb + g] = s;
+    else static_cast<uint8_t*>(a.xs)[m * a.Kb + g] = static_cast<uint8_t>(sbyte);
+  } else if (FMT == 0) {
+    static_cast<float*>(a.xs)[g * a.ld_s + m] = s;
+  } else {
+    uint8_t* t = static_cast<uint8_t*>(a.xs) + sf_tile_offset(m, g, a.Kq);
+    *t = static_cast<uint8_t>(sbyte);
+    if (g == a.Kb - 1)
+      for (int j = g + 1; (j & 3) != 0; ++j) *++t = 127u;
+  }
+}
+
+// Rows past the last token of a scale-factor tile: 2^0 in every slot.
+__device__ __forceinline__ void pad_scales(const NormActArgs& a, int64_t m, int from, int step) {
+  for (int q = from; q < a.Kq; q += step)
+    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.xs) + sf_tile_offset(m, 4 * q, a.Kq)) = 0x7F7F7F7Fu;
+}
+
 // A lane's 8 channels k .. k + 7 of token m, as n = -v (quantize_negated):
 // the group's amax over its lanes (a.group / 8 neighbours), scale, codes, and
 // v in bf16 on request.  Every lane of the warp calls it (lanes without
@@ -72,11 +97,7 @@ __device__ __forceinline__ void quantize_lane(const NormActArgs& a, const float2
   if (!real) return;
   *reinterpret_cast<uint2*>(a.xq + m * a.K + k) = make_uint2(q[0], q[1]);
   if (a.y != nullptr) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + m * a.ld_y + k) = flip_signs(pack8(n));
-  if ((k & (a.group - 1)) == 0) {
-    const int64_t g = m * a.Kb + (k >> a.group_shift);
-    if (FMT == 0) static_cast<float*>(a.xs)[g] = s;
-    else static_cast<uint8_t*>(a.xs)[g] = static_cast<uint8_t>(sbyte);
-  }
+  if ((k & (a.group - 1)) == 0) store_scale<FMT, false>(a, m, k >> a.group_shift, s, sbyte);
 }
 
 __device__ __forceinline__ float square_sum(const float2 (&z)[4], float ss) {
@@ -128,6 +149,7 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_row_kernel(const NormActArgs 
   grid_launch_dependents();
   const int t = threadIdx.x;
   const int64_t m = blockIdx.x;
+  if (m >= a.M) return pad_scales(a, m, t, THREADS);
   const int steps = (a.K + 8 * THREADS - 1) / (8 * THREADS);
   auto load = [&](int i, float2 (&z)[4]) {
     const int k = 8 * (t + i * THREADS);
@@ -226,11 +248,11 @@ __device__ __forceinline__ void store_channels(uint16_t* p, const float2 (&f)[8]
   *reinterpret_cast<uint4*>(p + 8) = FLIP ? flip_signs(b) : b;
 }
 
-// quantize_lane for 16 channels (a group is 8, 4 or 2 lanes), with the places
-// of its outputs: xq the lane's codes, xs its group's scale (in elements).
-template <int FMT>
-__device__ __forceinline__ void quantize_channels(const NormActArgs& a, const float2 (&n)[8], uint8_t* xq, int64_t xs,
-                                                  uint16_t* y, bool lead, bool real) {
+// quantize_lane for 16 channels (a group is 8, 4 or 2 lanes); `lead`: the
+// lane stores its group's scale.
+template <int FMT, bool ROW>
+__device__ __forceinline__ void quantize_channels(const NormActArgs& a, const float2 (&n)[8], int64_t m, int k,
+                                                  bool lead, bool real) {
   float amax = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(n[i].x), fabsf(n[i].y)));
@@ -242,24 +264,22 @@ __device__ __forceinline__ void quantize_channels(const NormActArgs& a, const fl
   uint32_t q[4];
   quantize_negated<FMT, 8>(n, s, sbyte, q);
   if (!real) return;
-  *reinterpret_cast<uint4*>(xq) = make_uint4(q[0], q[1], q[2], q[3]);
-  if (a.y != nullptr) store_channels<true>(y, n);
-  if (lead) {
-    if (FMT == 0) static_cast<float*>(a.xs)[xs] = s;
-    else static_cast<uint8_t*>(a.xs)[xs] = static_cast<uint8_t>(sbyte);
-  }
+  *reinterpret_cast<uint4*>(a.xq + m * a.K + k) = make_uint4(q[0], q[1], q[2], q[3]);
+  if (a.y != nullptr) store_channels<true>(static_cast<uint16_t*>(a.y) + m * a.ld_y + k, n);
+  if (lead) store_scale<FMT, ROW>(a, m, k >> a.group_shift, s, sbyte);
 }
 
 // RMS norm: a team of W warps per token (up to 32 / W tokens at a time),
 // whose weight stays in registers; the team's sum of squares meets in shared
 // memory at the team's own barrier.
-constexpr int rms_warps(int S) { return S == 1 ? 32 : 24; }
+// warps of a CTA at most: rings of four two-operand items leave room for 24
+constexpr int rms_warps(int S, int OPS, int NBUF) { return S == 2 || OPS * NBUF == 8 ? 24 : 32; }
 
-template <int FMT, int S, int OPS, int NBUF>
-__global__ void __launch_bounds__(rms_warps(S) * 32, 1) rmsnorm_stream_kernel(const NormActArgs a, const int W) {
+template <int FMT, int S, int OPS, int NBUF, bool ROW>
+__global__ void __launch_bounds__(rms_warps(S, OPS, NBUF) * 32, 1) rmsnorm_stream_kernel(const NormActArgs a, const int W) {
   constexpr int kItem = S * OPS * 1024;
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float red[2][rms_warps(S)];
+  __shared__ float red[2][32];
   grid_wait_prerequisites();
   grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -342,20 +362,20 @@ __global__ void __launch_bounds__(rms_warps(S) * 32, 1) rmsnorm_stream_kernel(co
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         z[s][j] = __fmul2_rn(__fmul2_rn(z[s][j], make_float2(-rstd, -rstd)), j < 4 ? lo[j & 3] : hi[j & 3]);
-      quantize_channels<FMT>(a, z[s], a.xq + static_cast<int64_t>(m) * a.K + k,
-                             static_cast<int64_t>(m) * a.Kb + (k >> a.group_shift),
-                             static_cast<uint16_t*>(a.y) + m * a.ld_y + k, lead, real);
+      quantize_channels<FMT, ROW>(a, z[s], m, k, lead, real);
     }
     buf = buf + 1 == NBUF ? 0 : buf + 1;
     ahead = ahead + 1 == NBUF ? 0 : ahead + 1;
   }
+  if (!ROW && a.layout == kScaleSfTiles)
+    for (int m = a.M + blockIdx.x; m < a.M_pad; m += gridDim.x) pad_scales(a, m, threadIdx.x, blockDim.x);
 }
 
 // silu(gate) * up: an item is 512 channels of a token (the last of a token
 // may be shorter).
 constexpr int kSiluWarps = 32, kSiluBuffers = 3;
 
-template <int FMT>
+template <int FMT, bool ROW>
 __global__ void __launch_bounds__(kSiluWarps * 32, 1) silu_mul_stream_kernel(const NormActArgs a, const int per_row,
                                                                              const int64_t items) {
   constexpr int kItem = 2048, NBUF = kSiluBuffers;
@@ -415,12 +435,13 @@ __global__ void __launch_bounds__(kSiluWarps * 32, 1) silu_mul_stream_kernel(con
     lds_channels(src + 1024, lp, real, u);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = silu_mul2<true>(v[j], u[j]);
-    quantize_channels<FMT>(a, v, a.xq + mo * a.K + k, mo * a.Kb + (k >> a.group_shift),
-                           static_cast<uint16_t*>(a.y) + mo * a.ld_y + k, lead, real);
+    quantize_channels<FMT, ROW>(a, v, mo, k, lead, real);
     step(mo, jo);
     buf = buf + 1 == NBUF ? 0 : buf + 1;
     ahead = ahead + 1 == NBUF ? 0 : ahead + 1;
   }
+  if (!ROW && a.layout == kScaleSfTiles)
+    for (int m = a.M + blockIdx.x; m < a.M_pad; m += gridDim.x) pad_scales(a, m, threadIdx.x, blockDim.x);
 }
 
 template <int FMT>
@@ -440,8 +461,12 @@ __global__ void __launch_bounds__(128) silu_mul_row_kernel(const NormActArgs a, 
   grid_wait_prerequisites();
   grid_launch_dependents();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (i >= items) return;
   const int64_t m = i / per_row;
+  if (a.layout == kScaleSfTiles && m >= a.M) {  // items past the tokens' own: one per padding row and 256 channels
+    if (m < a.M_pad) pad_scales(a, m, static_cast<int>(i - m * per_row) * 32 + (threadIdx.x & 31), per_row * 32);
+    return;
+  }
+  if (i >= items) return;
   const int k = static_cast<int>(i - m * per_row) * 256 + (threadIdx.x & 31) * 8;
   const bool real = k < a.K;
   uint4 g = make_uint4(0u, 0u, 0u, 0u), u = g;
@@ -471,17 +496,20 @@ cudaError_t launch_stream(void (*kern)(P...), std::atomic<uint64_t>& configured,
 
 template <int FMT, int S, int OPS, int NBUF>
 cudaError_t rms_stream(const NormActArgs& a, int W, int warps, cudaLaunchConfig_t& cfg) {
-  static std::atomic<uint64_t> configured{0};
+  static std::atomic<uint64_t> configured[2];
   if (warps * NBUF * S * OPS * 1024 > kStreamSmem) return cudaErrorInvalidValue;
-  return launch_stream(rmsnorm_stream_kernel<FMT, S, OPS, NBUF>, configured, warps, cfg, a, W);
+  if (a.layout == kScaleRowMajor)
+    return launch_stream(rmsnorm_stream_kernel<FMT, S, OPS, NBUF, true>, configured[0], warps, cfg, a, W);
+  return launch_stream(rmsnorm_stream_kernel<FMT, S, OPS, NBUF, false>, configured[1], warps, cfg, a, W);
 }
 
 template <int FMT>
 cudaError_t launch_rms(const NormActArgs& a, int num_sms, cudaLaunchConfig_t& cfg) {
   const int n = (a.K + 511) / 512;  // steps of 512 channels in a row
   const int S = n <= 32 ? 1 : 2, W = (n + S - 1) / S;
-  if (W <= rms_warps(S)) {
-    const int teams = rms_warps(S) / W, warps = teams * W;
+  const int most = S == 1 ? 32 : 24;
+  if (W <= most) {
+    const int teams = most / W, warps = teams * W;
     // A team's ring pays from a few tokens on; below that the one-row kernel
     // has more loads in flight.  us, stream / row kernel, float scales: with
     // a residual 600 x 12288 (4 a team) 13 / 12, 1200 x 7168 (4) 15 / 17,
@@ -496,7 +524,7 @@ cudaError_t launch_rms(const NormActArgs& a, int num_sms, cudaLaunchConfig_t& cf
       return warps <= 24 ? rms_stream<FMT, 1, 2, 4>(a, W, warps, cfg) : rms_stream<FMT, 1, 2, 3>(a, W, warps, cfg);
     }
   }
-  cfg.gridDim = dim3(static_cast<unsigned>(a.M));
+  cfg.gridDim = dim3(static_cast<unsigned>(a.layout == kScaleSfTiles ? a.M_pad : a.M));
 #define FG8_RMS(T, C) \
   { cfg.blockDim = dim3(T); return cudaLaunchKernelEx(&cfg, rmsnorm_row_kernel<FMT, T, C>, a); }
   if (a.K <= 256) FG8_RMS(32, 1)
@@ -516,14 +544,17 @@ cudaError_t launch_silu(const NormActArgs& a, int num_sms, cudaLaunchConfig_t& c
   // us, stream / row kernel, float scales: 512 x 14336 (3 items a warp) 10.4 /
   // 9.2, 1024 x 14336 (6) 16.6 / 16.8, 8192 x 2048 (7) 16.9 / 19.0
   if (static_cast<int64_t>(a.M) * per_row >= static_cast<int64_t>(6) * num_sms * kSiluWarps) {
-    static std::atomic<uint64_t> configured{0};
+    static std::atomic<uint64_t> configured[2];
+    const int64_t items = static_cast<int64_t>(a.M) * per_row;
     cfg.gridDim = dim3(static_cast<unsigned>(num_sms));
-    return launch_stream(silu_mul_stream_kernel<FMT>, configured, kSiluWarps, cfg, a, per_row,
-                         static_cast<int64_t>(a.M) * per_row);
+    if (a.layout == kScaleRowMajor)
+      return launch_stream(silu_mul_stream_kernel<FMT, true>, configured[0], kSiluWarps, cfg, a, per_row, items);
+    return launch_stream(silu_mul_stream_kernel<FMT, false>, configured[1], kSiluWarps, cfg, a, per_row, items);
   }
   const int row = (a.K + 255) / 256;
   const int64_t items = static_cast<int64_t>(a.M) * row;
-  cfg.gridDim = dim3(static_cast<unsigned>((items + 3) / 4));
+  const int64_t warps = a.layout == kScaleSfTiles ? static_cast<int64_t>(a.M_pad) * row : items;
+  cfg.gridDim = dim3(static_cast<unsigned>((warps + 3) / 4));
   cfg.blockDim = dim3(128);
   return cudaLaunchKernelEx(&cfg, silu_mul_row_kernel<FMT>, a, row, items);
 }

@@ -76,7 +76,7 @@ __device__ __forceinline__ float ex2_approx(float x) {  // 2^x, relative error 2
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float rcp_approx(float x) {  // 1 / x within one ulp (x in [1, 2] here)
+__device__ __forceinline__ float rcp_approx(float x) {  // 1 / x within one ulp, x and 1 / x normal
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
@@ -115,17 +115,18 @@ __device__ __forceinline__ float group_scale_fast(float amax) {
 
 // Codes of values v that float32 arithmetic made (not of given bf16 values),
 // which come NEGATED, n = -v.  The quotient takes one FMA correction of
-// q0 = v RN(1/s): q1 = q0 - (q0 s - v) RN(1/s), which is v / s exactly where
-// that is a float32, so ties between two codes are kept, and before its
-// rounding within 2^-23 ulp of it otherwise.  With n in place of v both steps
-// are plain FMAs, and a zero keeps its sign without being given it: for
-// v = -0 the correction is (+0)(-y) + (-0) = -0.
+// q0 = v y, y the approximate 1/s: q1 = q0 - (q0 s - v) y.  q0 is within 3 ulp
+// of v / s, so the correction is right to 2^-21 ulp before q1's rounding: q1
+// is v / s where that is a float32 (ties between two codes are kept) and next
+// to correctly rounded otherwise.  With n in place of v both steps are plain
+// FMAs, and a zero keeps its sign without being given it: for v = -0 the
+// correction is (+0)(-y) + (-0) = -0.
 template <int FMT, int N>
 __device__ __forceinline__ void quantize_negated(const float2 (&n)[N], float s, uint32_t sbyte,
                                                  uint32_t (&codes)[N / 2]) {
   float2 q[N];
   if (FMT == 0) {
-    const float y = -__frcp_rn(s);
+    const float y = -rcp_approx(s);
     const float2 Y = make_float2(y, y), S = make_float2(s, s);
 #pragma unroll
     for (int i = 0; i < N; ++i) {

@@ -407,6 +407,69 @@ def silu_mul_quant(gate: torch.Tensor, up: torch.Tensor, scale_fmt="float", bloc
     return xq, xs, y
 
 
+def _linear_operands(x: torch.Tensor, wq, w_scale_inv, bias, fmt: int, out, workspace):
+    """The weight side of rmsnorm_linear and silu_mul_linear for input rows x: (N, bias pointer, y, workspace)."""
+    M, K = x.shape
+    if not isinstance(wq, torch.Tensor) or wq.dim() != 2:
+        raise ValueError("wq must be [N, K]")
+    N = int(wq.shape[0])
+    _check_weight(wq, w_scale_inv, (), N, K, fmt, 128, x.device)
+    bp = _check_bias(bias, (N,), x.device)
+    y = _output(out, M, N, x.device)
+    _check_cuda(x, "x")
+    return N, bp, y, _workspace(C.fg8_linear_workspace_bytes(M, N, K, fmt), x.device, workspace)
+
+
+def rmsnorm_linear(x: torch.Tensor, weight: torch.Tensor, wq: torch.Tensor, w_scale_inv: torch.Tensor,
+                   bias: Optional[torch.Tensor] = None, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
+                   scale_fmt="float", residual_out: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """linear on the RMS norm of x (+ residual): rmsnorm_quant's codes and scales go straight into the
+    linear's workspace.  Returns (y [M, N] bf16, bf16(x + residual) or None without a residual).
+    residual_out may be `residual` itself; workspace as for linear."""
+    fmt = scale_fmt_code(scale_fmt)
+    _check_bf16_matrix(x, "x")
+    M, K = x.shape
+    _check_tensor(weight, "weight", (K,), (torch.bfloat16,), x.device)
+    if residual is not None:
+        _check_like(residual, "residual", x)
+    if residual_out is not None:
+        if residual is None:
+            raise ValueError("residual_out needs a residual")
+        _check_like(residual_out, "residual_out", x)
+    N, bp, y, ws = _linear_operands(x, wq, w_scale_inv, bias, fmt, out, workspace)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    nb, s = ws.numel() * ws.element_size(), _stream(x)
+    with _on(x.device):
+        C.fg8_linear_prepare_rmsnorm(x.data_ptr(), M, N, K, x.stride(0), 0 if residual is None else residual.data_ptr(),
+                                     K if residual is None else residual.stride(0), weight.data_ptr(), eps,
+                                     0 if residual_out is None else residual_out.data_ptr(),
+                                     K if residual_out is None else residual_out.stride(0), 0, K,
+                                     w_scale_inv.data_ptr(), fmt, ws.data_ptr(), nb, s)
+        C.fg8_linear_run(wq.data_ptr(), w_scale_inv.data_ptr(), bp, y.data_ptr(), M, N, K, y.stride(0), fmt,
+                         ws.data_ptr(), nb, s)
+    return y, residual_out
+
+
+def silu_mul_linear(gate: torch.Tensor, up: torch.Tensor, wq: torch.Tensor, w_scale_inv: torch.Tensor,
+                    bias: Optional[torch.Tensor] = None, scale_fmt="float", out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """linear on silu(gate) * up: silu_mul_quant's codes and scales go straight into the linear's workspace."""
+    fmt = scale_fmt_code(scale_fmt)
+    _check_bf16_matrix(gate, "gate")
+    _check_like(up, "up", gate)
+    M, K = gate.shape
+    N, bp, y, ws = _linear_operands(gate, wq, w_scale_inv, bias, fmt, out, workspace)
+    nb, s = ws.numel() * ws.element_size(), _stream(gate)
+    with _on(gate.device):
+        C.fg8_linear_prepare_silu_mul(gate.data_ptr(), up.data_ptr(), M, N, K, gate.stride(0), up.stride(0),
+                                      w_scale_inv.data_ptr(), fmt, ws.data_ptr(), nb, s)
+        C.fg8_linear_run(wq.data_ptr(), w_scale_inv.data_ptr(), bp, y.data_ptr(), M, N, K, y.stride(0), fmt,
+                         ws.data_ptr(), nb, s)
+    return y
+
+
 def moe_route(logits: torch.Tensor, k: int, renormalize: bool = True,
               scale: float = 1.0) -> Tuple[torch.Tensor, torch.Tensor]:
     """Expert routing: logits [T, E] float32 or bf16 -> (ids int32 [T, k], weights

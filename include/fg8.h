@@ -415,6 +415,27 @@ FG8_API fg8_status fg8_silu_mul_quant(const void* gate_bf16, const void* up_bf16
                                       int64_t ld_gate, int64_t ld_up, void* xq_e4m3, void* x_scale,
                                       fg8_scale_fmt fmt, int block, void* y_bf16, int64_t ld_y, void* stream);
 
+/* fg8_rmsnorm_quant / fg8_silu_mul_quant as the first half of a linear:
+ * they take fg8_linear_prepare's place (128-wide groups) and write the codes
+ * and scales into fg8_linear's workspace in the layouts that fg8_linear_run
+ * reads, so that
+ *   fg8_linear_prepare_rmsnorm(...);  fg8_linear_run(...);
+ * is norm, quantization and the linear (few-token or tiled kernel, by shape)
+ * in two launches with float scales (three with UE8M0, which also packs
+ * w_scale_inv).  The same codes and scales as the stand-alone forms.  Operands
+ * and checks as there; K, N, w_scale_inv and the workspace
+ * (fg8_linear_workspace_bytes(M, N, K, fmt)) as fg8_linear_prepare. */
+FG8_API fg8_status fg8_linear_prepare_rmsnorm(const void* x_bf16, int64_t M, int64_t N, int64_t K, int64_t ld_x,
+                                              const void* residual_bf16, int64_t ld_residual,
+                                              const void* weight_bf16, float eps, void* residual_out_bf16,
+                                              int64_t ld_residual_out, void* y_bf16, int64_t ld_y,
+                                              const void* w_scale_inv, fg8_scale_fmt fmt, void* workspace,
+                                              size_t workspace_bytes, void* stream);
+FG8_API fg8_status fg8_linear_prepare_silu_mul(const void* gate_bf16, const void* up_bf16, int64_t M, int64_t N,
+                                               int64_t K, int64_t ld_gate, int64_t ld_up, const void* w_scale_inv,
+                                               fg8_scale_fmt fmt, void* workspace, size_t workspace_bytes,
+                                               void* stream);
+
 /* Expert routing: for each token the k largest of its E logits in falling
  * order (equal logits: the lowest index first) and their softmax weights,
  *   weights[t, j] = scale * exp(l_j - l_max) / sum,

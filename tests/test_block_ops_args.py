@@ -62,6 +62,31 @@ def test_silu_mul_refusals(raw):
     assert c(M=0, g=None) == 0
 
 
+def test_prepare_refusals(raw):
+    c = _caller(raw.fg8_linear_prepare_rmsnorm,
+                "x M N K ld_x r ld_r w eps ro ld_ro y ld_y ws fmt wsp nb stream".split(),
+                dict(x=FAKE, M=40, N=256, K=256, ld_x=256, r=None, ld_r=0, w=FAKE, eps=1e-6, ro=None, ld_ro=0, y=None,
+                     ld_y=0, ws=FAKE, fmt=1, wsp=FAKE, nb=BIG, stream=None))
+    for bad in (dict(fmt=3), dict(M=-1), dict(M=(1 << 31) - 1), dict(N=0), dict(ld_x=128), dict(eps=0.0), dict(x=None),
+                dict(w=None), dict(ws=None), dict(r=FAKE, ld_r=256), dict(y=FAKE, ld_y=128)):
+        assert c(**bad) == 1, bad
+    for bad in (dict(N=252), dict(K=200), dict(x=FAKE + 8), dict(w=FAKE + 8), dict(y=FAKE + 8, ld_y=256)):
+        assert c(**bad) == 2, bad
+    for bad in (dict(wsp=None), dict(wsp=FAKE + 64), dict(nb=1024)):
+        assert c(**bad) == 4, bad
+    assert c(M=0, x=None, wsp=None) == 0
+    d = _caller(raw.fg8_linear_prepare_silu_mul, "g u M N K ld_g ld_u ws fmt wsp nb stream".split(),
+                dict(g=FAKE, u=FAKE, M=40, N=256, K=256, ld_g=512, ld_u=512, ws=FAKE, fmt=0, wsp=FAKE, nb=BIG,
+                     stream=None))
+    for bad in (dict(fmt=-1), dict(g=None), dict(u=None), dict(ws=None), dict(ld_u=128), dict(K=0)):
+        assert d(**bad) == 1, bad
+    for bad in (dict(N=4), dict(K=248), dict(ld_g=516), dict(u=FAKE + 8)):
+        assert d(**bad) == 2, bad
+    assert d(nb=2048) == 4 and d(M=0, g=None) == 0
+    if not torch.cuda.is_available():
+        assert c() == 3 and d() == 3
+
+
 def test_route_refusals(raw):
     c = _caller(raw.fg8_moe_route, "l bf16 T E ld k renorm scale ids w stream".split(),
                 dict(l=FAKE, bf16=0, T=4, E=64, ld=64, k=8, renorm=1, scale=1.0, ids=FAKE, w=FAKE, stream=None))
@@ -118,6 +143,14 @@ def test_wrappers_name_the_operand():
     _raises("residual_out needs", n, x, w, residual_out=x)
     _raises("residual_out must be", n, x, w, 1e-6, x, residual_out=torch.zeros(4, 128, dtype=BF16))
     _raises("scale_fmt", n, x, w, 1e-6, None, "fp8")
+    wq, ws = torch.zeros(64, 256, dtype=E4M3), torch.zeros(1, 2)
+    _raises("x must be a CUDA tensor", fg8.rmsnorm_linear, x, w, wq, ws)
+    _raises("wq must have shape", fg8.rmsnorm_linear, x, w, wq[:, :128].contiguous(), ws)
+    _raises("weight must have shape", fg8.rmsnorm_linear, x, w[:8], wq, ws)
+    _raises("residual_out needs", fg8.rmsnorm_linear, x, w, wq, ws, residual_out=x)
+    _raises("x must be a CUDA tensor", fg8.silu_mul_linear, x, x, wq, ws)
+    _raises("up must be", fg8.silu_mul_linear, x, x[:2], wq, ws)
+    _raises("bias must have shape", fg8.silu_mul_linear, x, x, wq, ws, w)
     s = fg8.silu_mul_quant
     _raises("gate must be a CUDA tensor", s, x, x)
     _raises("up must be", s, x, x[:, :128])

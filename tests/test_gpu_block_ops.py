@@ -41,7 +41,8 @@ def _same(a, b):
 @pytest.mark.parametrize("M,K,block,residual", [
     (1, 16, 128, True), (3, 48, 32, False), (2, 512, 128, True), (5, 528, 64, True), (7, 1024, 128, False),
     (4, 1040, 32, True), (1, 7168, 128, True), (33, 2064, 128, True), (130, 4096, 64, False), (2, 4112, 128, True),
-    (3, 8208, 128, True), (2, 12288, 128, True), (2, 12304, 64, True), (2, 24576, 128, False), (2, 24592, 32, True),
+    (3, 8208, 128, True), (600, 7168, 128, False), (1300, 4112, 64, True), (9500, 480, 32, True),
+    (300, 16400, 128, True), (2, 12288, 128, True), (2, 12304, 64, True), (2, 24576, 128, False), (2, 24592, 32, True),
     (1, 60000, 128, True), (1023, 256, 128, True)])
 def test_rmsnorm_quant(fg8, fmt, M, K, block, residual):
     x = W.x_outliers(M, K, seed=M + K).cuda()
@@ -128,6 +129,54 @@ def test_silu_mul_quant(fg8, fmt, M, K, block):
     assert bool(((y.to(F64) - v).abs() <= v.abs() * 2.0 ** -8 + err).all())
     a = fg8.silu_mul_quant(g.contiguous(), u.contiguous(), fmt, block=block)
     assert _same(a[0], xq) and _same(a[1], xs) and a[2] is None
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,K,N", [(1, 16, 8), (5, 400, 264), (33, 7168, 136), (130, 1040, 256), (600, 528, 512),
+                                   (9500, 480, 64), (1300, 4112, 72), (300, 16400, 64)])
+def test_prepare_forms(fg8, fmt, M, K, N):
+    """fg8_linear_prepare_rmsnorm / _silu_mul leave the stand-alone forms' codes and scales in the GEMM's layouts, and
+    the linears built on them give gemm_prequant's bits where both run the tiled GEMM, and the oracle's values
+    otherwise.  The workspace starts as noise behind its header: padding must not reach y."""
+    from _ws_layout import decode, offsets
+    code = fg8.scale_fmt_code(fmt)
+    x, r = W.x_outliers(M, K, seed=M + K).cuda(), W.normal((M, K), 1.0, seed=M).cuda()
+    nw = (1 + W.normal((K,), 0.3, seed=K).float()).to(BF16).cuda()
+    wq, ws = fg8.quantize_weight(W.normal((N, K), 0.05, seed=N).cuda(), fmt)
+    b = W.normal((N,), 0.1, seed=N + 1).cuda()
+    nb = fg8.fg8_linear_workspace_bytes(M, N, K, code)
+    for which in ("rmsnorm", "silu"):
+        wsp = torch.full((nb,), 0xA5, dtype=U8, device="cuda")
+        wsp[:1024] = 0
+        if which == "rmsnorm":
+            q, s, ro, _ = fg8.rmsnorm_quant(x, nw, 1e-6, r, fmt)
+            y, ro2 = fg8.rmsnorm_linear(x, nw, wq, ws, b, 1e-6, r, fmt, workspace=wsp)
+            assert torch.equal(ro, ro2)
+        else:
+            q, s, _ = fg8.silu_mul_quant(x, r, fmt)
+            y = fg8.silu_mul_linear(x, r, wq, ws, b, fmt, workspace=wsp)
+        torch.cuda.synchronize()
+        gq, gs = decode(wsp.cpu().numpy(), M, K, code)
+        assert np.array_equal(gq, q.view(U8).cpu().numpy()), which
+        want = s.cpu().numpy().view(np.uint32) if code == 0 else s.view(U8).cpu().numpy()
+        assert np.array_equal(gs, want), which
+        if code == 1:  # the tiles' other entries are 2^0
+            xs_off, Kb = offsets(M, K)[1], (K + 127) // 128
+            rows, slots = (M + 127) // 128 * 128, (Kb + 3) // 4 * 4
+            t = wsp[xs_off:xs_off + rows * slots].cpu().numpy()
+            full = decode(np.concatenate([np.zeros(offsets(rows, slots * 128)[1], np.uint8), t]), rows, slots * 128, 1)[1]
+            assert (full[M:] == 127).all() and (full[:, Kb:] == 127).all()
+        if fg8.fg8_linear_plan(M, N, K, code)[0] == 0:
+            assert torch.equal(y, fg8.gemm_prequant(q, s, wq, ws, b, fmt)), which
+        else:
+            import oracle
+            from conftest import y_tolerance
+            ref, bound, _ = oracle.linear_dequant(gq, s.cpu().numpy() if code == 0 else gs, wq.view(U8).cpu().numpy(),
+                                                  ws.cpu().numpy() if code == 0 else ws.view(U8).cpu().numpy(),
+                                                  W.bf16_bits(b), code)
+            out = y.float().cpu().numpy().astype(np.float64)
+            assert np.all(np.abs(out - ref) <= y_tolerance(bound, ref, out)), which
+        assert fg8.fg8_check_device_status(wsp.data_ptr(), _s()) == 0
 
 
 def test_silu_mul_every_gate(fg8):
