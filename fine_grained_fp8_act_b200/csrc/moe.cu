@@ -41,6 +41,9 @@
 //
 // DOWN is launched to overlap UP's end: its first weight tiles are on their
 // way while UP's last units finish; only the warps that read h wait for it.
+// (Having UP's producers bring DOWN's first 5, 8 or 12 K-blocks per CTA into
+// L2 at their end changed nothing: 70.4 to 71.0 us against 70.4 for one token
+// over 8 experts of 7168 x 2048.)
 //
 // Every wait is bounded; on expiry the kernel records FG8_ERR_TIMEOUT in the
 // status word, drains its copies and tensor-core ops, frees TMEM and returns.
@@ -173,6 +176,7 @@ __device__ __forceinline__ void count_pairs(const MoeParams& p, const Routing& r
   for (int i = threadIdx.x; i < P; i += blockDim.x) {
     const int id = __ldg(p.ids + i);
     const bool on = id >= 0 && id < p.E;
+    if (p.weights != nullptr) prefetch_l1(p.weights + i);  // for the sums at the end
     r.ids[i] = on ? static_cast<uint16_t>(id) : static_cast<uint16_t>(0xFFFFu);
     if (on) atomicAdd(r.count + id, 1u);
     else if (id >= 0 && blockIdx.x == 0) atomicExch(p.status, kInvalidArgStatus);
@@ -225,15 +229,16 @@ __device__ __forceinline__ int place_pairs(const MoeParams& p, const Routing& r)
 // (total <= kMaxJobs * kMoeMaxInner K-blocks: 32 bits hold it)
 struct Walk {
   int left, total, run;  // K-blocks to go, of all CTAs; run: K-blocks per CTA where units stay whole, else 0
-  int ctas, jobs;
+  int ctas, jobs, Kb;
   // the current unit
   int job, e, tile, start, m, k0, k1;
   int begin;  // first K-block of the next unit
 
-  __device__ __forceinline__ Walk(const MoeParams& p, int njobs) {
+  __device__ __forceinline__ Walk(int tiles, int blocks, int njobs) {
     jobs = njobs;
-    const int grid = gridDim.x, units = jobs * p.tiles;
-    total = units * p.Kb;
+    Kb = blocks;
+    const int grid = gridDim.x, units = jobs * tiles;
+    total = units * Kb;
     // Whole units: the longest run has n of them, and the CTAs beside it
     // leave it more of the bandwidth (one CTA alone streams a K-block in 0.60
     // us, all 148 together in 0.73).  Equal runs: total / grid, and putting
@@ -241,7 +246,7 @@ struct Walk {
     // experts (56 K-blocks, 128 + 224 units): 80 us whole, 85 us cut; 2
     // experts with 8 units of 8 K-blocks: 24 and 22 us.
     const int n = (units + grid - 1) / grid;
-    run = static_cast<int64_t>(n) * p.Kb * 5 <= (static_cast<int64_t>(total / grid) + 6) * 6 ? n * p.Kb : 0;
+    run = static_cast<int64_t>(n) * Kb * 5 <= (static_cast<int64_t>(total / grid) + 6) * 6 ? n * Kb : 0;
     if (run > 0) {
       ctas = (units + n - 1) / n;
     } else {
@@ -252,8 +257,8 @@ struct Walk {
     if (static_cast<int>(blockIdx.x) < ctas) {
       const int w = begin_of(blockIdx.x);
       left = begin_of(blockIdx.x + 1) - w;
-      const int u = w / p.Kb;  // the unit before the first, for next() to step from
-      begin = w - u * p.Kb;
+      const int u = w / Kb;  // the unit before the first, for next() to step from
+      begin = w - u * Kb;
       tile = u / jobs;
       job = u - tile * jobs - 1;
     }
@@ -266,13 +271,13 @@ struct Walk {
   __device__ __forceinline__ int cta_of(int x) const {
     return run > 0 ? x / run : static_cast<int>((static_cast<int64_t>(x + 1) * ctas - 1) / total);
   }
-  __device__ __forceinline__ int first_block(const MoeParams& p) const { return (tile * jobs + job) * p.Kb; }
+  __device__ __forceinline__ int first_block() const { return (tile * jobs + job) * Kb; }
 
-  __device__ __forceinline__ bool next(const MoeParams& p, const Routing& r) {
+  __device__ __forceinline__ bool next(const Routing& r) {
     if (left <= 0) return false;
     k0 = begin;
     begin = 0;
-    k1 = left < p.Kb - k0 ? k0 + left : p.Kb;
+    k1 = left < Kb - k0 ? k0 + left : Kb;
     left -= k1 - k0;
     if (++job == jobs) {
       job = 0;
@@ -317,7 +322,7 @@ __device__ __forceinline__ void moe_producer(const CUtensorMap* tmW, const MoePa
                                              const Bars& b, Walk walk) {
   int64_t it = 0;
   bool ok = true;
-  while (ok && walk.next(p, r)) {
+  while (ok && walk.next(r)) {
     const int row0 = box_row<C>(p, walk.e, walk.tile, 0), row1 = box_row<C>(p, walk.e, walk.tile, 1);
     const bool second = has_second<C>(p, walk.tile);
     for (int kb = walk.k0; kb < walk.k1; ++kb, ++it) {
@@ -348,7 +353,7 @@ __device__ __forceinline__ void moe_mma(const MoeParams& p, const Routing& r, ui
     ok = false;
   }
   uint32_t it = 0;
-  while (ok && walk.next(p, r)) {
+  while (ok && walk.next(r)) {
     const uint32_t idesc = C::kIdesc | (uint32_t(walk.m <= 16 ? 2 : 4) << 17);
     for (int kb = walk.k0; kb < walk.k1; ++kb, ++it) {
       const uint32_t slot = it % C::STAGES, phase = (it / C::STAGES) & 1u;
@@ -387,7 +392,7 @@ __device__ __forceinline__ void moe_fill(const MoeParams& p, const Routing& r, u
   // pair / k as a product: pair < 2^12 and k <= 2^5 leave an error below 2^-8
   const uint32_t inv_k = ((1u << 20) + p.k - 1) / p.k;
   uint32_t it = 0;
-  while (walk.next(p, r)) {
+  while (walk.next(r)) {
     for (int kb = walk.k0; kb < walk.k1; ++kb, ++it) {
       if (static_cast<int>(it % C::kFillWarps) != fw) continue;
       const uint32_t ss = it % C::kSlots, sphase = ((it / C::kSlots) & 1u) ^ 1u;
@@ -641,8 +646,8 @@ __device__ __forceinline__ void combine(const MoeParams& p, int tile, int et) {
 
 // Counts an arrival on *counter after this CTA's epilogue stores; true for
 // every epilogue thread of the CTA that brings it to `want` (which zeroes it
-// for the next call).  The barrier orders the threads' stores before the one
-// thread's fence and atomic, and its second fence before their loads.
+// for the next call).  The barriers put the threads' stores in front of the
+// one thread's atomic and their loads behind it; it releases and acquires.
 template <class C>
 __device__ __forceinline__ bool arrive_last(uint32_t* counter, uint32_t want, int et, volatile int* flag) {
   if (want == 1u) {
@@ -651,9 +656,7 @@ __device__ __forceinline__ bool arrive_last(uint32_t* counter, uint32_t want, in
   }
   named_barrier_sync(1, C::kEpiThreads);
   if (et == 0) {
-    __threadfence();
-    const uint32_t done = atomicAdd(counter, 1u) + 1u;
-    __threadfence();
+    const uint32_t done = atomic_add_acq_rel(counter, 1u) + 1u;
     *flag = done == want ? 1 : 0;
     if (done == want) *counter = 0u;
   }
@@ -675,7 +678,7 @@ __device__ __forceinline__ void moe_epilogue(const MoeParams& p, const Routing& 
   float* stage = reinterpret_cast<float*>(smem + C::kOffStage);
   uint32_t it = 0;
   bool ok = true;
-  while (walk.next(p, r)) {
+  while (walk.next(r)) {
     float acc[kChunk];
 #pragma unroll
     for (int c = 0; c < kChunk; ++c) acc[c] = 0.0f;
@@ -702,7 +705,7 @@ __device__ __forceinline__ void moe_epilogue(const MoeParams& p, const Routing& 
     bool whole = true;
     CutUnit cu{0, 0};
     if (cut) {  // partial sums, added up by the last of the unit's CTAs
-      const int b0 = walk.first_block(p);
+      const int b0 = walk.first_block();
       cu.first = walk.cta_of(b0);
       cu.last = walk.cta_of(b0 + p.Kb - 1);
       float* mine = p.split + (2 * blockIdx.x + (static_cast<int>(blockIdx.x) == cu.first ? 1 : 0)) * kPartFloats;
@@ -810,7 +813,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const int jobs = *jobs_slot;
   if (jobs > 0) {
-    const Walk walk(p, jobs);
+    const Walk walk(p.tiles, p.Kb, jobs);
     if (warp == 0) {
       if (lane == 0) moe_producer<C>(&tmW, p, r, smem, b, walk);
     } else if (warp == 1) {
@@ -849,18 +852,24 @@ EncodeTiledFnMoe encode_fn_moe() {
   return fn;
 }
 
-template <class C>
-cudaError_t launch_phase(const MoeParams& p, const uint8_t* w, int64_t rows, int num_sms, cudaStream_t s) {
+// Every expert's rows as one e4m3 matrix [rows, K]: 128 x 128 boxes, 128-byte swizzle.
+cudaError_t weight_map(CUtensorMap* map, const uint8_t* w, int64_t rows, int K) {
   const EncodeTiledFnMoe fn = encode_fn_moe();
   if (fn == nullptr) return cudaErrorInvalidValue;
-  CUtensorMap tmW;  // every expert's rows as one e4m3 matrix [rows, K]: 128 x 128 boxes, 128-byte swizzle
   const cuuint32_t estr[2] = {1, 1}, box[2] = {128, 128};
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.K), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.K)};
-  if (fn(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(w), dims, strides, box, estr,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return cudaErrorInvalidValue;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K)};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(w), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+template <class C>
+cudaError_t launch_phase(const MoeParams& p, const uint8_t* w, int64_t rows, int num_sms, cudaStream_t s) {
+  CUtensorMap tmW;
+  if (const cudaError_t e = weight_map(&tmW, w, rows, p.K); e != cudaSuccess) return e;
   auto kern = moe_kernel<C>;
   // the shared-memory opt-in, once per device
   static std::atomic<uint64_t> configured{0};
@@ -935,6 +944,7 @@ cudaError_t launch_moe_mlp(const MoeArgs& a, int fmt, int num_sms, cudaStream_t 
   down.Kb = Ib;
   down.Nb = Hb;
   down.tiles = (a.H + kRowTile - 1) / kRowTile;
+  up.weights = nullptr;  // only DOWN sums
   return fmt == 0 ? launch_fmt<0>(a, up, down, num_sms, s) : launch_fmt<1>(a, up, down, num_sms, s);
 }
 
