@@ -61,7 +61,8 @@ def _scale_dtypes(fmt: int):
 def _check_bf16_matrix(t: torch.Tensor, name: str):
     if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D bf16 tensor")
-    if t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+    (rows, cols), (ld, unit) = t.shape, t.stride()
+    if unit != 1 or (rows > 1 and ld < cols):
         raise ValueError(f"{name} must have unit stride in its last dimension and rows that do not overlap")
 
 
