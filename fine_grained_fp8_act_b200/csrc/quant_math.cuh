@@ -82,28 +82,30 @@ __device__ __forceinline__ float rcp_approx(float x) {  // 1 / x within one ulp,
   return y;
 }
 
-// silu(g) * u for two values, in float32.  With e = exp(-|g|), silu(g) is
-// g / (1 + e) for g >= 0 and g e / (1 + e) below: the denominator lies in
-// [1, 2], so nothing overflows and the approximate reciprocal is good to an
-// ulp.  e = 2^t with t = -|g| log2(e) carried as a float and its remainder,
-// 2^(hi + lo) = 2^hi (1 + lo ln 2): the remainder would cost |g| 2^-25 of e
-// otherwise.  About 11 2^-24 relative in all; |g| e below 88 2^-126 becomes 0.
-// NEG: the negated value.
+// silu(g) * u for two values, in float32: g / (1 + e) * u with e = exp(-g) =
+// 2^t.  t = -g log2(e) is carried as a float and its remainder, t = hn - 2 r,
+// and 2^t = 2^hn (1 - 2 r ln 2): the remainder would cost |g| 2^-25 of e
+// otherwise.  About 10 2^-24 relative in all: e 4 (2^-22) and 1/2 for its
+// factor, then the sum, the reciprocal (an ulp), two products.
+// No finite gate needs a clamp.  Below -88 e overflows to inf, times a
+// factor of either sign, and 1 / d is a zero; from -87.336 on, where 1 / d is
+// no normal float32, it is 0 already (all of silu's 88 2^-126 there).  Above
+// 88 e is 0 and its factor finite: r comes from g log2(e) / 2, which bf16's
+// largest values do not overflow.
+// NEG: the negated value, by the signs of the constants.
 template <bool NEG = false>
 __device__ __forceinline__ float2 silu_mul2(float2 g, float2 u) {
-  const float2 a = make_float2(-fabsf(g.x), -fabsf(g.y));
-  constexpr float kL = 1.44269502162933349609375f;  // log2(e), rounded to float32
-  constexpr float kLLo = 1.92596299112661746887e-8f;  // log2(e) - kL
-  constexpr float kLn2 = 0.693147180559945309417f;
-  const float2 L = make_float2(kL, kL), LLo = make_float2(kLLo, kLLo), N = make_float2(kLn2, kLn2);
-  const float2 hi = __fmul2_rn(a, L);
-  const float2 lo = __ffma2_rn(a, LLo, __ffma2_rn(a, L, make_float2(-hi.x, -hi.y)));
-  float2 e = make_float2(ex2_approx(hi.x), ex2_approx(hi.y));
-  e = __ffma2_rn(e, __fmul2_rn(lo, N), e);
-  const float2 d = __fadd2_rn(e, make_float2(1.0f, 1.0f));
-  const float2 n = __fmul2_rn(g, make_float2(g.x < 0.0f ? e.x : 1.0f, g.y < 0.0f ? e.y : 1.0f));
-  const float rx = rcp_approx(d.x), ry = rcp_approx(d.y);
-  return __fmul2_rn(__fmul2_rn(n, NEG ? make_float2(-rx, -ry) : make_float2(rx, ry)), u);
+  constexpr float kHalfL = 0.721347510814666748046875f;    // log2(e) / 2, rounded to float32
+  constexpr float kHalfLLo = 9.62981495558310593435e-9f;   // log2(e) / 2 - kHalfL
+  constexpr float k2Ln2 = NEG ? 1.386294361119890618834f : -1.386294361119890618834f;
+  constexpr float kOne = NEG ? -1.0f : 1.0f;
+  const float2 one = make_float2(kOne, kOne);
+  const float2 h = __fmul2_rn(g, make_float2(-kHalfL, -kHalfL));
+  const float2 hn = __fadd2_rn(h, h);
+  const float2 r = __ffma2_rn(g, make_float2(kHalfLLo, kHalfLLo), __ffma2_rn(g, make_float2(kHalfL, kHalfL), h));
+  const float2 e = make_float2(ex2_approx(hn.x), ex2_approx(hn.y));
+  const float2 d = __ffma2_rn(e, __ffma2_rn(r, make_float2(k2Ln2, k2Ln2), one), one);
+  return __fmul2_rn(__fmul2_rn(g, make_float2(rcp_approx(d.x), rcp_approx(d.y))), u);
 }
 
 // amax / 448 correctly rounded, as __fdiv_rn would give it (amax below 2^-98

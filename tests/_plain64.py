@@ -64,10 +64,10 @@ def rmsnorm(x, weight, eps, residual):
 
 
 def silu_mul(g, u):
-    """(v, |error|) of g e / (1 + e) or g / (1 + e) with e = exp(-|g|) by an exponential that is off by at most 2^-22
-    (4 U): 4 U and 1 U for e, which the quotient passes on at most whole, then the numerator, the denominator, its
-    reciprocal (an ulp, 2 U), the quotient and the product with u: 11 U.  Where e is below float32's normal range,
-    |g| > 126 ln 2 = 87.336, it may be 0: silu is then below 87.4 2^-126 < 1.03e-36 in size, and all of it is lost."""
+    """(v, |error|) of g / (1 + e) * u with e = exp(-g) by an exponential that is off by at most 2^-22 (4 U): 4 U and
+    1 U for e, which the quotient passes on at most whole, then the sum 1 + e, its reciprocal (an ulp, 2 U) and two
+    products: 9 U (11 U for a form that also multiplies by e).  Where 1 / (1 + e) is below float32's normal range,
+    g < -126 ln 2 = -87.336, it may be 0: silu is then below 87.4 2^-126 < 1.03e-36 in size, and all of it is lost."""
     g, u = g.to(F64), u.to(F64)
     v = g / (1.0 + torch.exp(-g)) * u
     return v, v.abs() * (U * 11) + (g < -87.336) * u.abs() * 1.03e-36

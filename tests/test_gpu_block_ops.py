@@ -193,6 +193,22 @@ def test_silu_mul_every_gate(fg8):
         assert bool(((y.to(F64) - v).abs() <= v.abs() * 2.0 ** -8 + err + 2.0 ** -134).all())
 
 
+@pytest.mark.parametrize("M", [3, 5000])
+def test_silu_mul_extreme_gates(fg8, M):
+    """Finite gates up to bf16's largest: silu is the gate itself above, zero below; nothing becomes NaN.  (M 5000:
+    the streaming kernel.)"""
+    K = 512
+    big = torch.tensor([3.3895e38, -3.3895e38, 2.4e38, -2.4e38, 1e30, -1e30, 89.0, -89.0, 88.0, -88.0, 0.0, -0.0,
+                        1e-38, -1e-38, 1e-40, -1e-40], dtype=BF16).repeat(K // 16)
+    g = big.repeat(M, 1).cuda()
+    u = torch.full((M, K), 2.0 ** -20, dtype=BF16, device="cuda")
+    for fmt in FMTS:
+        xq, xs, y = fg8.silu_mul_quant(g, u, fmt, return_y=True)
+        v, err = P.silu_mul(g, u)
+        P.check_quantized(xq, xs, v, err + 2.0 ** -149, fmt, 128)
+        assert bool(((y.to(F64) - v).abs() <= v.abs() * 2.0 ** -8 + err + 2.0 ** -134).all())
+
+
 # ------------------------------------------------------------------ route --
 def _route64(l, k, renormalize, scale):
     l = l.float().to(F64).cpu().numpy()
