@@ -242,11 +242,12 @@ struct Walk {
     // Whole units: the longest run has n of them, and the CTAs beside it
     // leave it more of the bandwidth (one CTA alone streams a K-block in 0.60
     // us, all 148 together in 0.73).  Equal runs: total / grid, and putting
-    // the cut units together, about 4 us or 6 K-blocks.  One token over 8
-    // experts (56 K-blocks, 128 + 224 units): 80 us whole, 85 us cut; 2
-    // experts with 8 units of 8 K-blocks: 24 and 22 us.
+    // the cut units together, 2 to 3 us or 4 K-blocks.  us, whole / cut, H x I
+    // of the experts reached: 8 of 7168 x 2048 70.3 / 72.3, 8 of 4096 x 14336
+    // 221 / 225, 49 of 2064 x 1424 89.6 / 94.0; 41 of 2048 x 1408 79.5 / 76.0,
+    // 3 of 2048 x 768 23.1 / 17.4, 2 of 1024 x 512 17.0 / 15.6.
     const int n = (units + grid - 1) / grid;
-    run = static_cast<int64_t>(n) * Kb * 5 <= (static_cast<int64_t>(total / grid) + 6) * 6 ? n * Kb : 0;
+    run = static_cast<int64_t>(n) * Kb * 5 <= (static_cast<int64_t>(total / grid) + 4) * 6 ? n * Kb : 0;
     if (run > 0) {
       ctas = (units + n - 1) / n;
     } else {
