@@ -472,7 +472,9 @@ FG8_API fg8_status fg8_moe_route(const void* logits, int logits_bf16, int64_t T,
  *            gets zeros)
  *   workspace >= fg8_moe_mlp_workspace_bytes, with the header rules of
  *            fg8_linear
- * T <= 256, k <= 32, T * k <= 4096, E <= 1024, H <= 16384, I <= 2^20,
+ * The reached experts' weights stream once for up to 32 slots per expert and
+ * again, out of L2, for every further 32: far above that fg8_grouped_linear
+ * is faster.  T <= 256, k <= 32, T * k <= 4096, E <= 1024, H <= 16384, I <= 2^20,
  * H % 16 == 0, I % 16 == 0, E * 2I + 256 and E * H + 256 <= 2^31 - 1.  T == 0 is a no-op. */
 FG8_API size_t fg8_moe_mlp_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, fg8_scale_fmt fmt);
 FG8_API fg8_status fg8_moe_mlp(const void* x, const void* x_scale, int64_t T, int64_t H, int64_t ld_x,
