@@ -521,3 +521,100 @@ def test_empty_batches(fg8):
     assert ids.shape == (0, 2)
     b = Layer(fg8, 1, 2, 4, 256, 128, "float", seed=1)
     assert fg8.moe_mlp(z, ids, wt, b.w13, b.s13, b.w2, b.s2, "float").shape == (0, 256)
+
+
+# ------------------------------------------------ what a caller may also do --
+@pytest.mark.parametrize("fmt", FMTS)
+def test_moe_mlp_most_pairs_and_experts(fg8, fmt):
+    """The limits on tokens x slots and on experts at once: 4096 pairs over 1024 experts, and over one."""
+    a = Layer(fg8, 256, 16, 1024, 64, 32, fmt, seed=1)
+    y = a.run(fg8)
+    a.check(y)
+    a.ids[:] = 1023
+    a.check(a.run(fg8))
+
+
+def test_moe_mlp_one_workspace_for_many_shapes(fg8):
+    """Layers of several shapes, and a dense linear, on one workspace in turn: its header is at rest between them."""
+    shapes = [(1, 2, 4, 256, 128, "float"), (60, 4, 8, 1040, 272, "ue8m0"), (7, 1, 3, 4096, 48, "float")]
+    layers = [Layer(fg8, *s, seed=11 + i) for i, s in enumerate(shapes)]
+    x = W.x_normal(16, 4096, seed=3).cuda()
+    wq, ws = fg8.quantize_weight(W.normal((1024, 4096), 0.02, seed=4).cuda(), "float")
+    n = max(fg8.fg8_moe_mlp_workspace_bytes(*s[:5], fg8.scale_fmt_code(s[5])) for s in shapes)
+    wsp = torch.zeros(max(n, fg8.fg8_linear_workspace_bytes(16, 1024, 4096, 0)), dtype=U8, device="cuda")
+    want = [a.run(fg8) for a in layers] + [fg8.linear(x, wq, ws)]
+    for _ in range(3):
+        for a, w in zip(layers, want):
+            assert torch.equal(a.run(fg8, workspace=wsp), w)
+            assert torch.equal(fg8.linear(x, wq, ws, workspace=wsp), want[-1])
+    assert fg8.fg8_check_device_status(wsp.data_ptr(), _s()) == 0
+
+
+@pytest.mark.parametrize("codes", [False, True])
+def test_moe_mlp_tokens_do_not_mix(fg8, codes):
+    """NaN in one token's input stays in that token's output; a token without a slot does not read its own."""
+    T, k, E, H, I = 20, 2, 3, 400, 272
+    a = Layer(fg8, T, k, E, H, I, "float", seed=8)
+    a.ids[11] = -1
+    y = a.run(fg8)
+    x = a.x.clone()
+    x[5], x[11] = float("nan"), float("inf")
+    kw = dict(x=x)
+    if codes:
+        xq, xs = fg8.quantize_act(a.x, "float")
+        xq = xq.clone()
+        xq.view(U8)[5], xq.view(U8)[11] = 0x7F, 0x7F
+        kw = dict(x=xq, x_scale=xs)
+    z = a.run(fg8, **kw)
+    keep = [t for t in range(T) if t != 5]
+    assert torch.equal(z[keep], y[keep]) and bool((z[11] == 0).all()) and bool(torch.isnan(z[5]).all())
+
+
+def test_moe_mlp_strided_rows(fg8):
+    T, k, E, H, I = 9, 2, 4, 272, 144
+    a = Layer(fg8, T, k, E, H, I, "ue8m0", seed=6)
+    want = a.run(fg8)
+    big = torch.zeros(T, H + 40, dtype=BF16, device="cuda")
+    xv = big[:, 24:24 + H]
+    xv.copy_(a.x)
+    out = torch.full((T, H + 8), 7.0, dtype=BF16, device="cuda")
+    y = a.run(fg8, x=xv, out=out[:, :H])
+    assert torch.equal(y, want) and bool((out[:, H:] == 7).all())
+
+
+def test_norm_rows_do_not_mix(fg8):
+    for M, K in ((6, 1040), (5000, 512), (1300, 4096)):
+        x, r = W.normal((M, K), 1.0, seed=1).cuda(), W.normal((M, K), 1.0, seed=2).cuda()
+        w = torch.ones(K, dtype=BF16, device="cuda")
+        want = fg8.rmsnorm_quant(x, w, 1e-6, r, "float")
+        x[M // 2, 3] = float("nan")
+        got = fg8.rmsnorm_quant(x, w, 1e-6, r, "float")
+        keep = torch.arange(M, device="cuda") != M // 2
+        for g, e in zip(got[:3], want[:3]):
+            assert _same(_bits(g)[keep], _bits(e)[keep])
+
+
+def test_norm_and_silu_past_32_bit_offsets(fg8):
+    """2.2e9 elements: the last rows' outputs lie past 2^31 elements and 2^32 bytes."""
+    M, K = 270000, 8192
+    x = torch.empty(M, K, dtype=BF16, device="cuda")
+    x[:-8] = 1.0
+    x[-8:] = W.x_outliers(8, K, seed=5).cuda()
+    w = (1 + W.normal((K,), 0.3, seed=6).float()).to(BF16).cuda()
+    xq, xs, _, _ = fg8.rmsnorm_quant(x, w, 1e-6, None, "float")
+    _, v, err = P.rmsnorm(x[-8:], w, float(np.float32(1e-6)), None)
+    P.check_quantized(xq[-8:], xs[-8:], v, err, "float", 128)
+    del xq, xs
+    xq, xs, _ = fg8.silu_mul_quant(x, x, "ue8m0", block=64)
+    v, err = P.silu_mul(x[-8:], x[-8:])
+    P.check_quantized(xq[-8:], xs[-8:], v, err, "ue8m0", 64)
+
+
+def test_unaligned_views_are_refused(fg8):
+    x = W.normal((8, 528), 1.0, seed=1).cuda()
+    w = torch.ones(512, dtype=BF16, device="cuda")
+    for call in (lambda: fg8.rmsnorm_quant(x[:, 4:516], w), lambda: fg8.silu_mul_quant(x[:, 4:516], x[:, :512]),
+                 lambda: fg8.rmsnorm_quant(x[:, :520], torch.ones(520, dtype=BF16, device="cuda"))):
+        with pytest.raises(fg8.FG8Error) as e:
+            call()
+        assert e.value.status == fg8.FG8_ERR_ALIGNMENT
