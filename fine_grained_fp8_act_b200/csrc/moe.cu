@@ -148,6 +148,12 @@ struct MoeCfg {
   static_assert((2 * STAGES + 3 * kSlots + 2) * 8 + 32 <= 512, "barrier area");
   // M = 128 weight rows, K-major e4m3 operands, f32 accumulate; N is added per unit
   static_assert(kSlots * kAccCols == 512, "TMEM columns");
+  // An activation warp that comes to K-block i last waited for i - kFillWarps
+  // - kSlots to be consumed, which with kFillWarps <= kSlots puts i - 2 kSlots
+  // behind it: the slot's barrier is at most one phase back, and the parity
+  // that the warp waits for is not that of an earlier phase.  (The one MMA
+  // issuer and the epilogue see every K-block.)
+  static_assert(kFillWarps <= kSlots, "phases told apart by their parity");
   static constexpr uint32_t kIdesc = (1u << 4) | (uint32_t(128 >> 4) << 24);
 };
 
