@@ -4,7 +4,8 @@
 //   h    = silu(gate) * up,   gate = W13[e][:I] . x[t],   up = W13[e][I:] . x[t]
 //
 // x and h are quantized per token in groups of 1 x 128 as the dense layers'
-// activations are; gate, up, h and the down products stay in float32 until
+// activations are (x inside the first kernel, or for many tokens an expert by
+// a launch in front of it, with the same codes); gate, up, h and the down products stay in float32 until
 // that quantization and until y's one rounding to bf16.
 //
 // With few tokens the layer is bound by reading the reached experts' e4m3
@@ -78,19 +79,29 @@ static_assert(kMaxGrid + kMoeMaxHidden / kRowTile <= kHeaderCounters, "counters 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 // [header | h codes [P, I] | h scales float32 [P, ceil(I/128)] | partial
-// sums of split units, two per CTA | down products float32 [P, H]]
+// sums of split units, two per CTA | down products float32 [P, H] | with
+// quantize_first: x's codes and scales]
 struct MoeWs {
-  size_t hq, hs, split, part, total;
+  size_t hq, hs, split, part, xq, xs, total;
 };
 
-MoeWs moe_ws_layout(int64_t T, int64_t k, int64_t H, int64_t I) {
+// Whether bf16 x is quantized by a launch of its own: every CTA that runs a
+// token's expert quantizes the token again, which from some 8 tokens an
+// expert on takes longer than the launch.  us, one / the other: 64 tokens,
+// top-8 of 64, 7168 x 2048 463 / 461; 64, top-2 of 8, 4096 x 14336 268 / 258;
+// 100, top-4 of 8, 4096 x 2048 110 / 100.
+bool quantize_first(int64_t T, int64_t k, int64_t E) { return T * k >= 8 * E; }
+
+MoeWs moe_ws_layout(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
   MoeWs w;
   const int64_t P = T * k, Ib = (I + 127) / 128;
   w.hq = kWorkspaceHeaderBytes;
   w.hs = align256(w.hq + P * I);
   w.split = align256(w.hs + P * Ib * 4);
   w.part = align256(w.split + 2 * kMaxGrid * kPartFloats * 4);
-  w.total = align256(w.part + P * H * 4);
+  w.xq = align256(w.part + P * H * 4);
+  w.xs = align256(w.xq + (quantize_first(T, k, E) ? T * H : 0));
+  w.total = align256(w.xs + (quantize_first(T, k, E) ? T * ((H + 127) / 128) * 4 : 0));
   return w;
 }
 
@@ -914,11 +925,28 @@ cudaError_t launch_fmt(const MoeArgs& a, const MoeParams& up, const MoeParams& d
 
 }  // namespace
 
-size_t moe_workspace_need(int T, int k, int E, int H, int I, int fmt) { return moe_ws_layout(T, k, H, I).total; }
+size_t moe_workspace_need(int T, int k, int E, int H, int I, int fmt) { return moe_ws_layout(T, k, E, H, I).total; }
 
 cudaError_t launch_moe_mlp(const MoeArgs& a, int fmt, int num_sms, cudaStream_t s) {
-  const MoeWs L = moe_ws_layout(a.T, a.k, a.H, a.I);
+  const MoeWs L = moe_ws_layout(a.T, a.k, a.E, a.H, a.I);
   const int Hb = (a.H + 127) / 128, Ib = (a.I + 127) / 128;
+  if (a.x_scale == nullptr && quantize_first(a.T, a.k, a.E)) {
+    ActQuantArgs q{};
+    q.x = a.x;
+    q.ld_x = a.ld_x;
+    q.M = a.T;
+    q.K = a.H;
+    q.Kb = Hb;
+    q.xq = a.ws + L.xq;
+    q.xs = a.ws + L.xs;
+    q.layout = kScaleRowMajor;
+    if (const cudaError_t e = launch_act_quant(q, fmt, num_sms, s); e != cudaSuccess) return e;
+    MoeArgs b = a;
+    b.x = q.xq;
+    b.ld_x = a.H;
+    b.x_scale = q.xs;
+    return launch_moe_mlp(b, fmt, num_sms, s);
+  }
   MoeParams p{};
   p.x = a.x;
   p.ld_x = a.ld_x;

@@ -525,7 +525,10 @@ def moe_mlp(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: torc
     _check_tensor(w13_scale_inv, "w13_scale_inv", (E, _cdiv(2 * I, 128), _cdiv(H, 128)), _scale_dtypes(fmt), x.device)
     _check_tensor(w2, "w2", (E, H, I), _E4M3, x.device)
     _check_tensor(w2_scale_inv, "w2_scale_inv", (E, _cdiv(H, 128), _cdiv(I, 128)), _scale_dtypes(fmt), x.device)
-    y = _output(out, T, H, x.device)
+    if out is None and x_scale is None:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    else:
+        y = _output(out, T, H, x.device)
     _check_cuda(x, "x")
     nbytes = C.fg8_moe_mlp_workspace_bytes(T, k, E, H, I, fmt)  # 0: the call below reports why
     ws = _workspace(nbytes, x.device, workspace)
