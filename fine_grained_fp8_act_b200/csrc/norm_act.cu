@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(rms_warps(S, OPS, NBUF) * 32, 1) rmsnorm_strea
     if (W > 1) {
       // two sets in turn: a warp ahead by one token writes the other one
       if (lane == 0) red[flip][warp] = sum;
-      named_barrier_sync(1 + team, W * 32);
+      named_barrier_sync(team, W * 32);  // at most 16 teams, 16 barriers: the CTA's own (0) is not used here
       sum = warp_sum(lane < W ? red[flip][team * W + lane] : 0.0f);
       flip ^= 1;
     }
@@ -509,7 +509,7 @@ cudaError_t launch_rms(const NormActArgs& a, int num_sms, cudaLaunchConfig_t& cf
   const int S = n <= 32 ? 1 : 2, W = (n + S - 1) / S;
   const int most = S == 1 ? 32 : 24;
   if (W <= most) {
-    const int teams = most / W, warps = teams * W;
+    const int teams = most / W, warps = teams * W;  // (16 teams at most where W > 1: 16 hardware barriers)
     // A team's ring pays from a few tokens on; below that the one-row kernel
     // has more loads in flight.  us, stream / row kernel, float scales: with
     // a residual 600 x 12288 (4 a team) 13 / 12, 1200 x 7168 (4) 15 / 17,

@@ -59,6 +59,23 @@ def test_rmsnorm_quant(fg8, fmt, M, K, block, residual):
         assert ro is None
 
 
+@pytest.mark.parametrize("residual", [True, False])
+@pytest.mark.parametrize("K,tokens", [(272, 32), (624, 16), (1024, 16), (1040, 10), (2048, 8), (2304, 6), (4096, 4),
+                                      (5632, 2), (8192, 2), (8208, 1), (16384, 1), (16400, 1), (24576, 1)])
+def test_rmsnorm_teams(fg8, K, tokens, residual):
+    """Enough rows for the streaming form at every number of tokens that a CTA works on side by side (32 down to 1,
+    up to one hardware barrier each): the last rows of the grid's last turn included."""
+    M = 4 * 148 * tokens + 5
+    x, w = W.normal((M, K), 2.0, seed=K).cuda(), W.normal((K,), 1.0, seed=K + 2).cuda()
+    r = W.normal((M, K), 2.0, seed=K + 1).cuda() if residual else None
+    xq, xs, ro, y = fg8.rmsnorm_quant(x, w, 1e-6, r, "float", return_y=True)
+    z, v, err = P.rmsnorm(x, w, float(np.float32(1e-6)), r)
+    P.check_quantized(xq, xs, v, err, "float", 128, "rmsnorm")
+    assert bool(((y.to(F64) - v).abs() <= v.abs() * 2.0 ** -8 + err).all())
+    if residual:
+        assert torch.equal(ro, (x.float() + r.float()).to(BF16))
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_rmsnorm_quant_of_bf16_steps(fg8, fmt):
     """Where v is exact in bf16 (rows of +-2^a with weights 2^b, so that the mean square is a power of two and
