@@ -40,7 +40,7 @@ _HERE = contextlib.nullcontext()
 
 def _on(device: torch.device):
     """torch.cuda.device(device), and nothing where that is the current device already."""
-    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return _HERE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
 def _cdiv(a: int, b: int) -> int:
@@ -58,12 +58,14 @@ def _scale_dtypes(fmt: int):
     return (torch.float32,) if fmt == C.FG8_SCALE_FLOAT else (torch.float8_e8m0fnu, torch.uint8)
 
 
-def _check_bf16_matrix(t: torch.Tensor, name: str):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 2:
+def _check_bf16_matrix(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
+    """(rows, columns, row stride)"""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D bf16 tensor")
     (rows, cols), (ld, unit) = t.shape, t.stride()
     if unit != 1 or (rows > 1 and ld < cols):
         raise ValueError(f"{name} must have unit stride in its last dimension and rows that do not overlap")
+    return rows, cols, ld
 
 
 def _check_cuda(t: torch.Tensor, name: str):
@@ -341,20 +343,39 @@ def scale_to_ue8m0(scale: torch.Tensor) -> Tuple[torch.Tensor, int]:
     return out.view(torch.float8_e8m0fnu), int(bad.item())
 
 
-def _quantized_outputs(x: torch.Tensor, fmt: int, block: int):
-    """e4m3 [M, K] and the scales' [M, ceil(K/block)] for bf16 rows x (rows apart or not: new tensors are contiguous)."""
+# The wrappers below serve single tokens too, where the kernel takes 2 to 4 us:
+# an operand's shape and stride are read once, outputs come from the cheapest
+# allocating call (empty_like, then new_empty with sizes spelled out).
+def _like(x: torch.Tensor, contiguous: bool, dtype=torch.bfloat16) -> torch.Tensor:
+    """A new contiguous tensor of x's shape."""
+    return (torch.empty_like(x, dtype=dtype) if contiguous else
+            torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format))
+
+
+def _check_block(block: int):
     if block not in (128, 64, 32):
         raise ValueError(f"block must be 128, 64 or 32, got {block!r}")
-    M, K = x.shape
-    return (torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format),
-            x.new_empty((M, _cdiv(K, block)), dtype=_SCALE_DTYPES[fmt]))
 
 
-def _check_like(t, name: str, x: torch.Tensor):
-    """t: bf16 rows of x's shape, on its device."""
-    _check_bf16_matrix(t, name)
-    if t.shape != x.shape or t.device != x.device:
-        raise ValueError(f"{name} must be {tuple(x.shape)} on {x.device}")
+def _check_like(t, name: str, M: int, K: int, device) -> int:
+    """t: bf16 rows [M, K] on device; their stride."""
+    rows, cols, ld = _check_bf16_matrix(t, name)
+    if rows != M or cols != K or t.device != device:
+        raise ValueError(f"{name} must be {(M, K)} on {device}")
+    return ld
+
+
+def _norm_operands(x, weight, residual, residual_out):
+    """Checks the norm's inputs: (M, K, row strides of x, residual and residual_out), K where there is none."""
+    M, K, ld = _check_bf16_matrix(x, "x")
+    device = x.device
+    _check_tensor(weight, "weight", (K,), (torch.bfloat16,), device)
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+        return M, K, ld, K, K
+    ld_r = _check_like(residual, "residual", M, K, device)
+    return M, K, ld, ld_r, K if residual_out is None else _check_like(residual_out, "residual_out", M, K, device)
 
 
 def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
@@ -367,26 +388,19 @@ def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, resi
     None): xq and x_scale are what gemm_prequant and moe_mlp take.  residual_out
     (default: a new tensor) may be `residual` itself, to update it in place."""
     fmt = scale_fmt_code(scale_fmt)
-    _check_bf16_matrix(x, "x")
-    M, K = x.shape
-    _check_tensor(weight, "weight", (K,), (torch.bfloat16,), x.device)
-    if residual is not None:
-        _check_like(residual, "residual", x)
-    if residual_out is not None:
-        if residual is None:
-            raise ValueError("residual_out needs a residual")
-        _check_like(residual_out, "residual_out", x)
+    M, K, ld, ld_r, ld_o = _norm_operands(x, weight, residual, residual_out)
+    _check_block(block)
     _check_cuda(x, "x")
-    xq, xs = _quantized_outputs(x, fmt, block)
+    packed = x.is_contiguous()
+    xq, xs = _like(x, packed, torch.float8_e4m3fn), x.new_empty(M, _cdiv(K, block), dtype=_SCALE_DTYPES[fmt])
     if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    y = torch.empty_like(x, memory_format=torch.contiguous_format) if return_y else None
+        residual_out = _like(x, packed)
+    y = _like(x, packed) if return_y else None
     with _on(x.device):
-        C.fg8_rmsnorm_quant(x.data_ptr(), M, K, x.stride(0), 0 if residual is None else residual.data_ptr(),
-                            K if residual is None else residual.stride(0), weight.data_ptr(), eps, xq.data_ptr(),
-                            xs.data_ptr(), fmt, block, 0 if residual_out is None else residual_out.data_ptr(),
-                            K if residual_out is None else residual_out.stride(0), 0 if y is None else y.data_ptr(),
-                            K, _stream(x))
+        C.fg8_rmsnorm_quant(x.data_ptr(), M, K, ld, 0 if residual is None else residual.data_ptr(), ld_r,
+                            weight.data_ptr(), eps, xq.data_ptr(), xs.data_ptr(), fmt, block,
+                            0 if residual is None else residual_out.data_ptr(), ld_o,
+                            0 if y is None else y.data_ptr(), K, _stream(x))
     return xq, xs, residual_out, y
 
 
@@ -396,15 +410,16 @@ def silu_mul_quant(gate: torch.Tensor, up: torch.Tensor, scale_fmt="float", bloc
     gate and up bf16 [M, K] (for instance y[:, :K] and y[:, K:] of one gate/up
     projection).  Returns (xq, x_scale, bf16(v) if return_y else None)."""
     fmt = scale_fmt_code(scale_fmt)
-    _check_bf16_matrix(gate, "gate")
-    _check_like(up, "up", gate)
+    M, K, ld = _check_bf16_matrix(gate, "gate")
+    ld_u = _check_like(up, "up", M, K, gate.device)
+    _check_block(block)
     _check_cuda(gate, "gate")
-    M, K = gate.shape
-    xq, xs = _quantized_outputs(gate, fmt, block)
-    y = torch.empty_like(gate, memory_format=torch.contiguous_format) if return_y else None
+    packed = gate.is_contiguous()
+    xq, xs = _like(gate, packed, torch.float8_e4m3fn), gate.new_empty(M, _cdiv(K, block), dtype=_SCALE_DTYPES[fmt])
+    y = _like(gate, packed) if return_y else None
     with _on(gate.device):
-        C.fg8_silu_mul_quant(gate.data_ptr(), up.data_ptr(), M, K, gate.stride(0), up.stride(0), xq.data_ptr(),
-                             xs.data_ptr(), fmt, block, 0 if y is None else y.data_ptr(), K, _stream(gate))
+        C.fg8_silu_mul_quant(gate.data_ptr(), up.data_ptr(), M, K, ld, ld_u, xq.data_ptr(), xs.data_ptr(), fmt, block,
+                             0 if y is None else y.data_ptr(), K, _stream(gate))
     return xq, xs, y
 
 
@@ -429,25 +444,15 @@ def rmsnorm_linear(x: torch.Tensor, weight: torch.Tensor, wq: torch.Tensor, w_sc
     linear's workspace.  Returns (y [M, N] bf16, bf16(x + residual) or None without a residual).
     residual_out may be `residual` itself; workspace as for linear."""
     fmt = scale_fmt_code(scale_fmt)
-    _check_bf16_matrix(x, "x")
-    M, K = x.shape
-    _check_tensor(weight, "weight", (K,), (torch.bfloat16,), x.device)
-    if residual is not None:
-        _check_like(residual, "residual", x)
-    if residual_out is not None:
-        if residual is None:
-            raise ValueError("residual_out needs a residual")
-        _check_like(residual_out, "residual_out", x)
+    M, K, ld, ld_r, ld_o = _norm_operands(x, weight, residual, residual_out)
     N, bp, y, ws = _linear_operands(x, wq, w_scale_inv, bias, fmt, out, workspace)
     if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        residual_out = _like(x, x.is_contiguous())
     nb, s = ws.numel() * ws.element_size(), _stream(x)
     with _on(x.device):
-        C.fg8_linear_prepare_rmsnorm(x.data_ptr(), M, N, K, x.stride(0), 0 if residual is None else residual.data_ptr(),
-                                     K if residual is None else residual.stride(0), weight.data_ptr(), eps,
-                                     0 if residual_out is None else residual_out.data_ptr(),
-                                     K if residual_out is None else residual_out.stride(0), 0, K,
-                                     w_scale_inv.data_ptr(), fmt, ws.data_ptr(), nb, s)
+        C.fg8_linear_prepare_rmsnorm(x.data_ptr(), M, N, K, ld, 0 if residual is None else residual.data_ptr(), ld_r,
+                                     weight.data_ptr(), eps, 0 if residual is None else residual_out.data_ptr(), ld_o,
+                                     0, K, w_scale_inv.data_ptr(), fmt, ws.data_ptr(), nb, s)
         C.fg8_linear_run(wq.data_ptr(), w_scale_inv.data_ptr(), bp, y.data_ptr(), M, N, K, y.stride(0), fmt,
                          ws.data_ptr(), nb, s)
     return y, residual_out
@@ -458,14 +463,13 @@ def silu_mul_linear(gate: torch.Tensor, up: torch.Tensor, wq: torch.Tensor, w_sc
                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """linear on silu(gate) * up: silu_mul_quant's codes and scales go straight into the linear's workspace."""
     fmt = scale_fmt_code(scale_fmt)
-    _check_bf16_matrix(gate, "gate")
-    _check_like(up, "up", gate)
-    M, K = gate.shape
+    M, K, ld = _check_bf16_matrix(gate, "gate")
+    ld_u = _check_like(up, "up", M, K, gate.device)
     N, bp, y, ws = _linear_operands(gate, wq, w_scale_inv, bias, fmt, out, workspace)
     nb, s = ws.numel() * ws.element_size(), _stream(gate)
     with _on(gate.device):
-        C.fg8_linear_prepare_silu_mul(gate.data_ptr(), up.data_ptr(), M, N, K, gate.stride(0), up.stride(0),
-                                      w_scale_inv.data_ptr(), fmt, ws.data_ptr(), nb, s)
+        C.fg8_linear_prepare_silu_mul(gate.data_ptr(), up.data_ptr(), M, N, K, ld, ld_u, w_scale_inv.data_ptr(), fmt,
+                                      ws.data_ptr(), nb, s)
         C.fg8_linear_run(wq.data_ptr(), w_scale_inv.data_ptr(), bp, y.data_ptr(), M, N, K, y.stride(0), fmt,
                          ws.data_ptr(), nb, s)
     return y
@@ -481,16 +485,16 @@ def moe_route(logits: torch.Tensor, k: int, renormalize: bool = True,
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or logits.dtype not in (torch.float32,
                                                                                          torch.bfloat16):
         raise ValueError("logits must be a 2-D float32 or bf16 tensor")
-    if logits.stride(1) != 1 or (logits.shape[0] > 1 and logits.stride(0) < logits.shape[1]):
+    (T, E), (ld, unit) = logits.shape, logits.stride()
+    if unit != 1 or (T > 1 and ld < E):
         raise ValueError("logits must have unit stride in its last dimension and rows that do not overlap")
-    T, E = logits.shape
     if not 1 <= k <= min(E, 32):
         raise ValueError(f"k must be between 1 and min({E}, 32), got {k}")
     _check_cuda(logits, "logits")
-    ids = logits.new_empty((T, k), dtype=torch.int32)
-    weights = logits.new_empty((T, k), dtype=torch.float32)
+    ids = logits.new_empty(T, k, dtype=torch.int32)
+    weights = torch.empty_like(ids, dtype=torch.float32)
     with _on(logits.device):
-        C.fg8_moe_route(logits.data_ptr(), 1 if logits.dtype == torch.bfloat16 else 0, T, E, logits.stride(0), k,
+        C.fg8_moe_route(logits.data_ptr(), 1 if logits.dtype is torch.bfloat16 else 0, T, E, ld, k,
                         1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), _stream(logits))
     return ids, weights
 
@@ -514,28 +518,25 @@ def moe_mlp(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: torc
         raise ValueError("w13 must be [E, 2I, H] and w2 [E, H, I]")
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
         raise ValueError("ids must be [T, k]")
-    (T, H), k = x.shape, int(ids.shape[1])
-    E, I = int(w13.shape[0]), int(w2.shape[2])
+    (T, H), k, E, I = x.shape, ids.shape[1], w13.shape[0], w2.shape[2]
+    device, scales, Hb = x.device, _scale_dtypes(fmt), _cdiv(H, 128)
     if x_scale is not None:
-        _check_tensor(x, "x", (T, H), _E4M3, x.device)
-        _check_tensor(x_scale, "x_scale", (T, _cdiv(H, 128)), _scale_dtypes(fmt), x.device)
-    _check_tensor(ids, "ids", (T, k), (torch.int32,), x.device)
-    _check_tensor(weights, "weights", (T, k), (torch.float32,), x.device)
-    _check_tensor(w13, "w13", (E, 2 * I, H), _E4M3, x.device)
-    _check_tensor(w13_scale_inv, "w13_scale_inv", (E, _cdiv(2 * I, 128), _cdiv(H, 128)), _scale_dtypes(fmt), x.device)
-    _check_tensor(w2, "w2", (E, H, I), _E4M3, x.device)
-    _check_tensor(w2_scale_inv, "w2_scale_inv", (E, _cdiv(H, 128), _cdiv(I, 128)), _scale_dtypes(fmt), x.device)
-    if out is None and x_scale is None:
-        y = torch.empty_like(x, memory_format=torch.contiguous_format)
-    else:
-        y = _output(out, T, H, x.device)
+        _check_tensor(x, "x", (T, H), _E4M3, device)
+        _check_tensor(x_scale, "x_scale", (T, Hb), scales, device)
+    _check_tensor(ids, "ids", (T, k), (torch.int32,), device)
+    _check_tensor(weights, "weights", (T, k), (torch.float32,), device)
+    _check_tensor(w13, "w13", (E, 2 * I, H), _E4M3, device)
+    _check_tensor(w13_scale_inv, "w13_scale_inv", (E, _cdiv(2 * I, 128), Hb), scales, device)
+    _check_tensor(w2, "w2", (E, H, I), _E4M3, device)
+    _check_tensor(w2_scale_inv, "w2_scale_inv", (E, Hb, _cdiv(I, 128)), scales, device)
+    y = _like(x, x.is_contiguous()) if out is None else _output(out, T, H, device)
     _check_cuda(x, "x")
     nbytes = C.fg8_moe_mlp_workspace_bytes(T, k, E, H, I, fmt)  # 0: the call below reports why
-    ws = _workspace(nbytes, x.device, workspace)
-    with _on(x.device):
+    ws = _workspace(nbytes, device, workspace)
+    with _on(device):
         C.fg8_moe_mlp(x.data_ptr(), 0 if x_scale is None else x_scale.data_ptr(), T, H, x.stride(0), ids.data_ptr(),
                       weights.data_ptr(), k, E, I, w13.data_ptr(), w13_scale_inv.data_ptr(), w2.data_ptr(),
-                      w2_scale_inv.data_ptr(), y.data_ptr(), y.stride(0), fmt, ws.data_ptr(),
+                      w2_scale_inv.data_ptr(), y.data_ptr(), H if out is None else y.stride(0), fmt, ws.data_ptr(),
                       ws.numel() * ws.element_size(), _stream(x))
     return y
 
