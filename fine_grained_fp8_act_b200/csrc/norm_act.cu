@@ -506,17 +506,23 @@ cudaError_t rms_stream(const NormActArgs& a, int W, int warps, cudaLaunchConfig_
 template <int FMT>
 cudaError_t launch_rms(const NormActArgs& a, int num_sms, cudaLaunchConfig_t& cfg) {
   const int n = (a.K + 511) / 512;  // steps of 512 channels in a row
-  const int S = n <= 32 ? 1 : 2, W = (n + S - 1) / S;
+  // Warps of one step each up to 32 of them; of two steps beyond, and where
+  // that lets two teams of ten or more work side by side instead of one: us,
+  // two steps / one, float scales, 16384 x 12288 with a residual 229 / 248,
+  // without 141 / 144; with one x 10240 197 / 210, but x 8720 193 / 186.
+  const int S = n <= 18 || (n > 24 && n <= 32) ? 1 : 2, W = (n + S - 1) / S;
   const int most = S == 1 ? 32 : 24;
   if (W <= most) {
     const int teams = most / W, warps = teams * W;  // (16 teams at most where W > 1: 16 hardware barriers)
     // A team's ring pays from a few tokens on; below that the one-row kernel
-    // has more loads in flight.  us, stream / row kernel, float scales: with
-    // a residual 600 x 12288 (4 a team) 13 / 12, 1200 x 7168 (4) 15 / 17,
-    // 2400 x 7168 (8) 26 / 41, 1200 x 4096 (2) 10 / 8, but 16384 x 512 (3)
-    // 10 / 18; without 600 x 7168 (2) 6.4 / 8.6, 300 x 7168 (1) 4.8 / 5.5.
-    const int64_t least = a.x2 == nullptr || n == 1 ? 2 : 4;
-    if (static_cast<int64_t>(a.M) >= least * num_sms * teams) {
+    // has more loads in flight.  us, stream / row kernel, float scales (tokens
+    // a team): without a residual 450 x 7168 (1.5) 4.8 / 6.7, 450 x 12288
+    // (1.5) 7.3 / 8.7, 900 x 4096 (1.5) 5.2 / 5.8, 1200 x 2048 (1) 4.8 / 3.9;
+    // with one 900 x 12288 (3) 17.6 / 17.2, 1200 x 12288 (4) 22.3 / 26.2,
+    // 1200 x 7168 (4) 14.2 / 15.9, 1800 x 4096 (3) 12.3 / 10.9, but 16384 x
+    // 512 (3) 10 / 18.
+    const int halves = n == 1 ? 4 : a.x2 == nullptr ? 3 : 8;
+    if (2 * static_cast<int64_t>(a.M) >= static_cast<int64_t>(halves) * num_sms * teams) {
       cfg.gridDim = dim3(static_cast<unsigned>(num_sms));
       if (a.x2 == nullptr)
         return S == 1 ? rms_stream<FMT, 1, 1, 4>(a, W, warps, cfg) : rms_stream<FMT, 2, 1, 4>(a, W, warps, cfg);
