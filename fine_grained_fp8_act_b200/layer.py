@@ -10,6 +10,7 @@ weight_scale_inv per 128x128 block shaped (ceil(out/128), ceil(in/128)),
 float32 or torch.float8_e8m0fnu for scale_fmt "ue8m0".
 """
 import contextlib
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -499,6 +500,12 @@ def moe_route(logits: torch.Tensor, k: int, renormalize: bool = True,
     return ids, weights
 
 
+@functools.lru_cache(maxsize=1024)
+def _moe_workspace_bytes(T: int, k: int, E: int, H: int, I: int, fmt: int) -> int:
+    """0 for a shape that fg8_moe_mlp refuses (it reports why)"""
+    return C.fg8_moe_mlp_workspace_bytes(T, k, E, H, I, fmt)
+
+
 def moe_mlp(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: torch.Tensor, w13_scale_inv: torch.Tensor,
             w2: torch.Tensor, w2_scale_inv: torch.Tensor, scale_fmt="ue8m0", x_scale: Optional[torch.Tensor] = None,
             out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -531,8 +538,7 @@ def moe_mlp(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: torc
     _check_tensor(w2_scale_inv, "w2_scale_inv", (E, Hb, _cdiv(I, 128)), scales, device)
     y = _like(x, x.is_contiguous()) if out is None else _output(out, T, H, device)
     _check_cuda(x, "x")
-    nbytes = C.fg8_moe_mlp_workspace_bytes(T, k, E, H, I, fmt)  # 0: the call below reports why
-    ws = _workspace(nbytes, device, workspace)
+    ws = _workspace(_moe_workspace_bytes(T, k, E, H, I, fmt), device, workspace)
     with _on(device):
         C.fg8_moe_mlp(x.data_ptr(), 0 if x_scale is None else x_scale.data_ptr(), T, H, x.stride(0), ids.data_ptr(),
                       weights.data_ptr(), k, E, I, w13.data_ptr(), w13_scale_inv.data_ptr(), w2.data_ptr(),
