@@ -249,7 +249,12 @@ def _route64(l, k, renormalize, scale):
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("T,E,k,renormalize", [(1, 1, 1, True), (3, 8, 2, True), (5, 8, 8, False), (130, 60, 4, True),
                                                (7, 64, 6, False), (1, 256, 8, True), (33, 160, 12, True),
-                                               (65, 384, 32, True), (4, 1024, 8, False), (9, 1000, 32, True)])
+                                               (65, 384, 32, True), (4, 1024, 8, False), (9, 1000, 32, True),
+                                               (6, 32, 5, True), (6, 33, 5, False), (6, 96, 6, True),
+                                               (6, 97, 6, False), (6, 128, 7, True), (6, 129, 7, True),
+                                               (6, 192, 8, False), (6, 193, 8, True), (6, 257, 8, True),
+                                               (6, 385, 9, True), (6, 512, 9, False), (6, 513, 9, True),
+                                               (6, 768, 10, True), (6, 769, 10, False)])
 def test_moe_route(fg8, dtype, T, E, k, renormalize):
     g = torch.Generator().manual_seed(T + E)
     l = (torch.randn(T, E, generator=g) * 3).to(dtype)
