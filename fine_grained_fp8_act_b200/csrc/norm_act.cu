@@ -288,13 +288,10 @@ __global__ void __launch_bounds__(rms_warps(S, OPS, NBUF) * 32, 1) rmsnorm_strea
   uint8_t* mine = ring + warp * NBUF * kItem;
   const int base = wt * S * 512;  // the warp's channels: S steps of 512
   const int k0 = base + lane * 16;
-  uint4 w[S][2];
-#pragma unroll
-  for (int s = 0; s < S; ++s) {
-    const int k = k0 + s * 512;
-    w[s][0] = k < a.K ? ldg16(a.weight, k) : make_uint4(0u, 0u, 0u, 0u);
-    w[s][1] = k < a.K ? ldg16(a.weight, k + 8) : make_uint4(0u, 0u, 0u, 0u);
-  }
+  // the weight of one step stays in registers; of two it would spill, and
+  // comes out of L1 for every token
+  uint4 held[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  if (S == 1 && k0 < a.K) held[0] = ldg16(a.weight, k0), held[1] = ldg16(a.weight, k0 + 8);
   // (M < 2^31 and the stride is at most 148 x 32: 32 unsigned bits hold both)
   const uint32_t stride = gridDim.x * teams, first = blockIdx.x * teams + team, M = a.M;
   uint32_t mi = first;  // the next token to copy
@@ -356,9 +353,11 @@ __global__ void __launch_bounds__(rms_warps(S, OPS, NBUF) * 32, 1) rmsnorm_strea
       const bool real = k0 + s * 512 < a.K;
       const int k = k0 + s * 512;
       if (OPS == 2 && real) store_channels<false>(static_cast<uint16_t*>(a.x2_out) + m * a.ld_x2_out + k, z[s]);
+      uint4 w[2] = {held[0], held[1]};
+      if (S > 1 && real) w[0] = ldg16(a.weight, k), w[1] = ldg16(a.weight, k + 8);
       float2 lo[4], hi[4];
-      unpack8(w[s][0], lo);
-      unpack8(w[s][1], hi);
+      unpack8(w[0], lo);
+      unpack8(w[1], hi);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         z[s][j] = __fmul2_rn(__fmul2_rn(z[s][j], make_float2(-rstd, -rstd)), j < 4 ? lo[j & 3] : hi[j & 3]);
@@ -506,23 +505,24 @@ cudaError_t rms_stream(const NormActArgs& a, int W, int warps, cudaLaunchConfig_
 template <int FMT>
 cudaError_t launch_rms(const NormActArgs& a, int num_sms, cudaLaunchConfig_t& cfg) {
   const int n = (a.K + 511) / 512;  // steps of 512 channels in a row
-  // Warps of one step each up to 32 of them; of two steps beyond, and where
-  // that lets two teams of ten or more work side by side instead of one: us,
-  // two steps / one, float scales, 16384 x 12288 with a residual 229 / 248,
-  // without 141 / 144; with one x 10240 197 / 210, but x 8720 193 / 186.
-  const int S = n <= 18 || (n > 24 && n <= 32) ? 1 : 2, W = (n + S - 1) / S;
+  // Two steps a warp: fewer shuffles and barriers a channel.  Up to eight
+  // steps it makes no difference, and for 25 to 32 there would be one team of
+  // 16 warps at most.  us, two steps / one, float scales, 16384 tokens with a
+  // residual and without: x 12288 216 / 248, 132 / 144; x 8192 148 / 153,
+  // 88 / 90; x 5632 105 / 109, 67 / 72; but x 6144 124 / 118, 67 / 73.
+  const int S = n <= 8 || (n > 24 && n <= 32) ? 1 : 2, W = (n + S - 1) / S;
   const int most = S == 1 ? 32 : 24;
   if (W <= most) {
     const int teams = most / W, warps = teams * W;  // (16 teams at most where W > 1: 16 hardware barriers)
-    // A team's ring pays from a few tokens on; below that the one-row kernel
-    // has more loads in flight.  us, stream / row kernel, float scales (tokens
-    // a team): without a residual 450 x 7168 (1.5) 4.8 / 6.7, 450 x 12288
-    // (1.5) 7.3 / 8.7, 900 x 4096 (1.5) 5.2 / 5.8, 1200 x 2048 (1) 4.8 / 3.9;
-    // with one 900 x 12288 (3) 17.6 / 17.2, 1200 x 12288 (4) 22.3 / 26.2,
-    // 1200 x 7168 (4) 14.2 / 15.9, 1800 x 4096 (3) 12.3 / 10.9, but 16384 x
-    // 512 (3) 10 / 18.
-    const int halves = n == 1 ? 4 : a.x2 == nullptr ? 3 : 8;
-    if (2 * static_cast<int64_t>(a.M) >= static_cast<int64_t>(halves) * num_sms * teams) {
+    // The rings pay from a few tokens on; below that the one-row kernel has
+    // more loads in flight.  Times of row kernel / stream, without and with a
+    // residual: two steps a warp (by tokens an SM) 300 x 7168 (2) 1.40, 1.12;
+    // 450 x 7168 (3) 1.21, 0.97; 300 x 12288 (2) 1.14, 0.88; 450 x 12288 (3)
+    // 1.42, 1.08; one step (by tokens a team) 900 x 4096 (1.5) 1.10, 0.81; 2400
+    // x 4096 (4) 1.37, 0.97; 3600 x 4096 (6) 1.51, 1.33; 2400 x 2048 (2) 1.00,
+    // 0.73; and 16384 x 512 with one (3) 1.8.
+    const int halves = S == 2 ? (a.x2 == nullptr ? 4 : 6) : (n == 1 ? 4 : a.x2 == nullptr ? 3 : 8) * teams;
+    if (2 * static_cast<int64_t>(a.M) >= static_cast<int64_t>(halves) * num_sms) {
       cfg.gridDim = dim3(static_cast<unsigned>(num_sms));
       if (a.x2 == nullptr)
         return S == 1 ? rms_stream<FMT, 1, 1, 4>(a, W, warps, cfg) : rms_stream<FMT, 2, 1, 4>(a, W, warps, cfg);

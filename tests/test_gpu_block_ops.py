@@ -61,8 +61,8 @@ def test_rmsnorm_quant(fg8, fmt, M, K, block, residual):
 
 @pytest.mark.parametrize("residual", [True, False])
 @pytest.mark.parametrize("K,tokens", [(272, 32), (624, 16), (1024, 16), (1040, 10), (2048, 8), (2304, 6), (4096, 4),
-                                      (5632, 2), (8192, 2), (8208, 1), (9232, 2), (12288, 2), (12304, 1), (16384, 1), (16400, 1),
-                                      (24576, 1)])
+                                      (4112, 4), (5632, 4), (6160, 3), (8192, 3), (8208, 2), (9232, 2), (12288, 2),
+                                      (12304, 1), (16384, 1), (16400, 1), (24576, 1)])
 def test_rmsnorm_teams(fg8, K, tokens, residual):
     """Enough rows for the streaming form at every number of tokens that a CTA works on side by side (32 down to 1,
     up to one hardware barrier each): the last rows of the grid's last turn included."""
