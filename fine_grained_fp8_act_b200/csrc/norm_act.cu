@@ -269,9 +269,8 @@ __device__ __forceinline__ void quantize_channels(const NormActArgs& a, const fl
   if (lead) store_scale<FMT, ROW>(a, m, k >> a.group_shift, s, sbyte);
 }
 
-// RMS norm: a team of W warps per token (up to 32 / W tokens at a time),
-// whose weight stays in registers; the team's sum of squares meets in shared
-// memory at the team's own barrier.
+// RMS norm: a team of W warps per token (up to 32 / W tokens at a time); the
+// team's sum of squares meets in shared memory at the team's own barrier.
 // warps of a CTA at most: rings of four two-operand items leave room for 24
 constexpr int rms_warps(int S, int OPS, int NBUF) { return S == 2 || OPS * NBUF == 8 ? 24 : 32; }
 
@@ -288,8 +287,9 @@ __global__ void __launch_bounds__(rms_warps(S, OPS, NBUF) * 32, 1) rmsnorm_strea
   uint8_t* mine = ring + warp * NBUF * kItem;
   const int base = wt * S * 512;  // the warp's channels: S steps of 512
   const int k0 = base + lane * 16;
-  // the weight of one step stays in registers; of two it would spill, and
-  // comes out of L1 for every token
+  // the weight of one step stays in registers; of two it would spill (48 to 92
+  // bytes: 16384 x 12288 with a residual 229 us), and comes out of L1 for
+  // every token (216)
   uint4 held[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
   if (S == 1 && k0 < a.K) held[0] = ldg16(a.weight, k0), held[1] = ldg16(a.weight, k0 + 8);
   // (M < 2^31 and the stride is at most 148 x 32: 32 unsigned bits hold both)
