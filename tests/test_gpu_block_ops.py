@@ -633,6 +633,23 @@ def test_norm_and_silu_past_32_bit_offsets(fg8):
     P.check_quantized(xq[-8:], xs[-8:], v, err, "ue8m0", 64)
 
 
+def test_moe_mlp_weights_past_32_bit_offsets(fg8):
+    """160 experts, 4.7e9 bytes of gate and up weights: the last ones' results are those of a layer of just them."""
+    E, H, I = 160, 7168, 2048
+    a = Layer(fg8, 3, 2, 3, H, I, "float", seed=9)
+    at = torch.tensor([0, E - 2, E - 1], device="cuda")
+    b = Layer.__new__(Layer)
+    b.fmt, b.E, b.x, b.w, b.ids = a.fmt, E, a.x, a.w, at[a.ids.long()].to(I32)
+    for name in ("w13", "s13", "w2", "s2"):
+        few = getattr(a, name)
+        many = torch.zeros((E, *few.shape[1:]), dtype=U8 if few.element_size() == 1 else few.dtype, device="cuda")
+        many[at] = _bits(few)
+        setattr(b, name, many.view(few.dtype))
+    y = a.run(fg8)
+    a.check(y)
+    assert torch.equal(b.run(fg8), y)
+
+
 def test_unaligned_views_are_refused(fg8):
     x = W.normal((8, 528), 1.0, seed=1).cuda()
     w = torch.ones(512, dtype=BF16, device="cuda")
