@@ -108,11 +108,16 @@ __device__ __forceinline__ float2 silu_mul2(float2 g, float2 u) {
   return __fmul2_rn(__fmul2_rn(g, make_float2(rcp_approx(d.x), rcp_approx(d.y))), u);
 }
 
-// amax / 448 correctly rounded, as __fdiv_rn would give it (amax below 2^-98
-// ends at the floor either way; above, every step is exact or normal).
+// group_scale without the division: amax / 448 correctly rounded wherever
+// that is a normal float32, since the remainder amax - q 448 is then a multiple
+// of 2^-149 below 2^24 of them, exact down to q = 2^-126 (amax = 2^-117.2);
+// smaller quotients end at the floor.  An infinite amax (a product past
+// float32) stays infinite: its remainder would be NaN, and the floor in its
+// place would turn the group into next to nothing.
 __device__ __forceinline__ float group_scale_fast(float amax) {
   constexpr float kInv = 1.0f / 448.0f;  // RN(1 / 448)
-  return fmaxf(div_rn_from_rcp(amax, 448.0f, kInv), kMinScale);
+  const float s = fmaxf(div_rn_from_rcp(amax, 448.0f, kInv), kMinScale);
+  return amax < __int_as_float(0x7f800000) ? s : amax;
 }
 
 // Codes of values v that float32 arithmetic made (not of given bf16 values),
