@@ -66,3 +66,58 @@ def test_rmsnorm_value_past_float32(fg8, fmt, M, K, block):
     clean = fg8.rmsnorm_quant(x * (torch.arange(M, device="cuda") != m)[:, None], w, 1e-6, None, fmt, block=block)
     got = fg8.rmsnorm_quant(x, w, 1e-6, None, fmt, block=block, return_y=True)
     _check_overflowed(fg8, fmt, got, clean, got[3], m, block)
+
+
+# -------------------------------------- silu(gate) * up, its streaming form --
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,K,block", [(30001, 480, 128), (3300, 4112, 64), (1700, 8208, 32), (28500, 16, 128)])
+def test_silu_mul_stream(fg8, fmt, M, K, block):
+    """Sizes past the few-token kernel's (six items of 512 channels a warp of the whole GPU)."""
+    both = W.normal((M, 2 * K), 3.0, seed=M + K).cuda()
+    both[:, ::37] *= 30
+    g, u = both[:, :K], both[:, K:]
+    xq, xs, y = fg8.silu_mul_quant(g, u, fmt, block=block, return_y=True)
+    v, err = P.silu_mul(g, u)
+    P.check_quantized(xq, xs, v, err, fmt, block, "silu_mul")
+    # gates of -90 and below leave v under 2^-126, where bf16's steps are all 2^-133: half of one beside the 2^-8
+    assert bool(((y.to(F64) - v).abs() <= v.abs() * 2.0 ** -8 + err + 2.0 ** -134).all())
+    # a row's results do not depend on how many rows there are: the few-token kernel's bits
+    few = fg8.silu_mul_quant(g[-9:], u[-9:], fmt, block=block, return_y=True)
+    for a, b in zip((xq, xs, y), few):
+        assert _same(a[-9:], b)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,K,N", [(30001, 480, 64), (3300, 4112, 72), (10007, 1040, 64)])
+def test_prepare_forms_streamed(fg8, fmt, M, K, N):
+    """The streaming kernels with their scales in the GEMM's layouts, against gemm_prequant on the row-major ones."""
+    code = fg8.scale_fmt_code(fmt)
+    x, r = W.x_outliers(M, K, seed=M + K).cuda(), W.normal((M, K), 1.0, seed=M).cuda()
+    nw = (1 + W.normal((K,), 0.3, seed=K).float()).to(BF16).cuda()
+    wq, ws = fg8.quantize_weight(W.normal((N, K), 0.05, seed=N).cuda(), fmt)
+    wsp = torch.full((fg8.fg8_linear_workspace_bytes(M, N, K, code),), 0xA5, dtype=U8, device="cuda")
+    wsp[:1024] = 0
+    q, s, ro, _ = fg8.rmsnorm_quant(x, nw, 1e-6, r, fmt)
+    y, ro2 = fg8.rmsnorm_linear(x, nw, wq, ws, None, 1e-6, r, fmt, workspace=wsp)
+    assert torch.equal(ro, ro2) and torch.equal(y, fg8.gemm_prequant(q, s, wq, ws, None, fmt))
+    q, s, ro, _ = fg8.rmsnorm_quant(x, nw, 1e-6, None, fmt)
+    y, _ = fg8.rmsnorm_linear(x, nw, wq, ws, None, 1e-6, None, fmt, workspace=wsp)
+    assert torch.equal(y, fg8.gemm_prequant(q, s, wq, ws, None, fmt))
+    q, s, _ = fg8.silu_mul_quant(x, r, fmt)
+    y = fg8.silu_mul_linear(x, r, wq, ws, None, fmt, workspace=wsp)
+    assert torch.equal(y, fg8.gemm_prequant(q, s, wq, ws, None, fmt))
+    assert fg8.fg8_check_device_status(wsp.data_ptr(), _s()) == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_silu_mul_extreme_gates_streamed(fg8, fmt):
+    """Finite gates up to bf16's largest in the streaming kernel: zeros below, the gate itself above, no NaN."""
+    M, K = 29000, 512
+    big = torch.tensor([3.3895e38, -3.3895e38, 2.4e38, -2.4e38, 1e30, -1e30, 89.0, -89.0, 88.0, -88.0, 0.0, -0.0,
+                        1e-38, -1e-38, 1e-40, -1e-40], dtype=BF16).repeat(K // 16)
+    g = big.repeat(M, 1).cuda()
+    u = torch.full((M, K), 2.0 ** -20, dtype=BF16, device="cuda")
+    xq, xs, y = fg8.silu_mul_quant(g, u, fmt, return_y=True)
+    v, err = P.silu_mul(g, u)
+    P.check_quantized(xq, xs, v, err + 2.0 ** -149, fmt, 128)
+    assert bool(((y.to(F64) - v).abs() <= v.abs() * 2.0 ** -8 + err + 2.0 ** -134).all())
