@@ -60,13 +60,18 @@ def _scale_dtypes(fmt: int):
 
 
 def _check_bf16_matrix(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
-    """(rows, columns, row stride)"""
+    """(rows, columns, row stride; the columns where there is one row, whose stride may be anything)"""
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D bf16 tensor")
     (rows, cols), (ld, unit) = t.shape, t.stride()
     if unit != 1 or (rows > 1 and ld < cols):
         raise ValueError(f"{name} must have unit stride in its last dimension and rows that do not overlap")
-    return rows, cols, ld
+    return rows, cols, ld if rows > 1 else cols
+
+
+def _ld(t: torch.Tensor) -> int:
+    """The row stride of a checked matrix, as _check_bf16_matrix gives it."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 def _check_cuda(t: torch.Tensor, name: str):
@@ -347,10 +352,9 @@ def scale_to_ue8m0(scale: torch.Tensor) -> Tuple[torch.Tensor, int]:
 # The wrappers below serve single tokens too, where the kernel takes 2 to 4 us:
 # an operand's shape and stride are read once, outputs come from the cheapest
 # allocating call (empty_like, then new_empty with sizes spelled out).
-def _like(x: torch.Tensor, contiguous: bool, dtype=torch.bfloat16) -> torch.Tensor:
-    """A new contiguous tensor of x's shape."""
-    return (torch.empty_like(x, dtype=dtype) if contiguous else
-            torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format))
+def _like(x: torch.Tensor, dtype=torch.bfloat16) -> torch.Tensor:
+    """A new row-major tensor of x's shape.  (Without the format one row would hand on its own stride, contiguous or not.)"""
+    return torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
 
 
 def _check_block(block: int):
@@ -392,11 +396,10 @@ def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, resi
     M, K, ld, ld_r, ld_o = _norm_operands(x, weight, residual, residual_out)
     _check_block(block)
     _check_cuda(x, "x")
-    packed = x.is_contiguous()
-    xq, xs = _like(x, packed, torch.float8_e4m3fn), x.new_empty(M, _cdiv(K, block), dtype=_SCALE_DTYPES[fmt])
+    xq, xs = _like(x, torch.float8_e4m3fn), x.new_empty(M, _cdiv(K, block), dtype=_SCALE_DTYPES[fmt])
     if residual is not None and residual_out is None:
-        residual_out = _like(x, packed)
-    y = _like(x, packed) if return_y else None
+        residual_out = _like(x)
+    y = _like(x) if return_y else None
     with _on(x.device):
         C.fg8_rmsnorm_quant(x.data_ptr(), M, K, ld, 0 if residual is None else residual.data_ptr(), ld_r,
                             weight.data_ptr(), eps, xq.data_ptr(), xs.data_ptr(), fmt, block,
@@ -415,9 +418,8 @@ def silu_mul_quant(gate: torch.Tensor, up: torch.Tensor, scale_fmt="float", bloc
     ld_u = _check_like(up, "up", M, K, gate.device)
     _check_block(block)
     _check_cuda(gate, "gate")
-    packed = gate.is_contiguous()
-    xq, xs = _like(gate, packed, torch.float8_e4m3fn), gate.new_empty(M, _cdiv(K, block), dtype=_SCALE_DTYPES[fmt])
-    y = _like(gate, packed) if return_y else None
+    xq, xs = _like(gate, torch.float8_e4m3fn), gate.new_empty(M, _cdiv(K, block), dtype=_SCALE_DTYPES[fmt])
+    y = _like(gate) if return_y else None
     with _on(gate.device):
         C.fg8_silu_mul_quant(gate.data_ptr(), up.data_ptr(), M, K, ld, ld_u, xq.data_ptr(), xs.data_ptr(), fmt, block,
                              0 if y is None else y.data_ptr(), K, _stream(gate))
@@ -448,14 +450,14 @@ def rmsnorm_linear(x: torch.Tensor, weight: torch.Tensor, wq: torch.Tensor, w_sc
     M, K, ld, ld_r, ld_o = _norm_operands(x, weight, residual, residual_out)
     N, bp, y, ws = _linear_operands(x, wq, w_scale_inv, bias, fmt, out, workspace)
     if residual is not None and residual_out is None:
-        residual_out = _like(x, x.is_contiguous())
+        residual_out = _like(x)
     nb, s = ws.numel() * ws.element_size(), _stream(x)
     with _on(x.device):
         C.fg8_linear_prepare_rmsnorm(x.data_ptr(), M, N, K, ld, 0 if residual is None else residual.data_ptr(), ld_r,
                                      weight.data_ptr(), eps, 0 if residual is None else residual_out.data_ptr(), ld_o,
                                      0, K, w_scale_inv.data_ptr(), fmt, ws.data_ptr(), nb, s)
-        C.fg8_linear_run(wq.data_ptr(), w_scale_inv.data_ptr(), bp, y.data_ptr(), M, N, K, y.stride(0), fmt,
-                         ws.data_ptr(), nb, s)
+        C.fg8_linear_run(wq.data_ptr(), w_scale_inv.data_ptr(), bp, y.data_ptr(), M, N, K, _ld(y), fmt, ws.data_ptr(),
+                         nb, s)
     return y, residual_out
 
 
@@ -471,8 +473,8 @@ def silu_mul_linear(gate: torch.Tensor, up: torch.Tensor, wq: torch.Tensor, w_sc
     with _on(gate.device):
         C.fg8_linear_prepare_silu_mul(gate.data_ptr(), up.data_ptr(), M, N, K, ld, ld_u, w_scale_inv.data_ptr(), fmt,
                                       ws.data_ptr(), nb, s)
-        C.fg8_linear_run(wq.data_ptr(), w_scale_inv.data_ptr(), bp, y.data_ptr(), M, N, K, y.stride(0), fmt,
-                         ws.data_ptr(), nb, s)
+        C.fg8_linear_run(wq.data_ptr(), w_scale_inv.data_ptr(), bp, y.data_ptr(), M, N, K, _ld(y), fmt, ws.data_ptr(),
+                         nb, s)
     return y
 
 
@@ -489,6 +491,8 @@ def moe_route(logits: torch.Tensor, k: int, renormalize: bool = True,
     (T, E), (ld, unit) = logits.shape, logits.stride()
     if unit != 1 or (T > 1 and ld < E):
         raise ValueError("logits must have unit stride in its last dimension and rows that do not overlap")
+    if T <= 1:
+        ld = E
     if not 1 <= k <= min(E, 32):
         raise ValueError(f"k must be between 1 and min({E}, 32), got {k}")
     _check_cuda(logits, "logits")
@@ -518,7 +522,7 @@ def moe_mlp(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: torc
     block scales.  For many tokens use grouped_linear."""
     fmt = scale_fmt_code(scale_fmt)
     if x_scale is None:
-        _check_bf16_matrix(x, "x")
+        ld = _check_bf16_matrix(x, "x")[2]
     elif not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be [T, H]")
     if not isinstance(w13, torch.Tensor) or not isinstance(w2, torch.Tensor) or w13.dim() != 3 or w2.dim() != 3:
@@ -529,6 +533,7 @@ def moe_mlp(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: torc
     device, scales, Hb = x.device, _scale_dtypes(fmt), _cdiv(H, 128)
     if x_scale is not None:
         _check_tensor(x, "x", (T, H), _E4M3, device)
+        ld = H
         _check_tensor(x_scale, "x_scale", (T, Hb), scales, device)
     _check_tensor(ids, "ids", (T, k), (torch.int32,), device)
     _check_tensor(weights, "weights", (T, k), (torch.float32,), device)
@@ -536,13 +541,13 @@ def moe_mlp(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: torc
     _check_tensor(w13_scale_inv, "w13_scale_inv", (E, _cdiv(2 * I, 128), Hb), scales, device)
     _check_tensor(w2, "w2", (E, H, I), _E4M3, device)
     _check_tensor(w2_scale_inv, "w2_scale_inv", (E, Hb, _cdiv(I, 128)), scales, device)
-    y = _like(x, x.is_contiguous()) if out is None else _output(out, T, H, device)
+    y = _like(x) if out is None else _output(out, T, H, device)
     _check_cuda(x, "x")
     ws = _workspace(_moe_workspace_bytes(T, k, E, H, I, fmt), device, workspace)
     with _on(device):
-        C.fg8_moe_mlp(x.data_ptr(), 0 if x_scale is None else x_scale.data_ptr(), T, H, x.stride(0), ids.data_ptr(),
+        C.fg8_moe_mlp(x.data_ptr(), 0 if x_scale is None else x_scale.data_ptr(), T, H, ld, ids.data_ptr(),
                       weights.data_ptr(), k, E, I, w13.data_ptr(), w13_scale_inv.data_ptr(), w2.data_ptr(),
-                      w2_scale_inv.data_ptr(), y.data_ptr(), H if out is None else y.stride(0), fmt, ws.data_ptr(),
+                      w2_scale_inv.data_ptr(), y.data_ptr(), _ld(y), fmt, ws.data_ptr(),
                       ws.numel() * ws.element_size(), _stream(x))
     return y
 

@@ -68,6 +68,64 @@ def test_rmsnorm_value_past_float32(fg8, fmt, M, K, block):
     _check_overflowed(fg8, fmt, got, clean, got[3], m, block)
 
 
+# ----------------------------------------------------------- one-row views --
+def _one_rows(K):
+    """One row at strides that are not its length: hidden[:, -1] of a batch of one, a buffer whose width is no
+    multiple of 8, a column's transpose."""
+    a = torch.zeros(3, 2 * K, dtype=BF16, device="cuda")[1:2, :K]
+    b = torch.zeros(1, K + 4, dtype=BF16, device="cuda")[:, :K]
+    c = torch.zeros(K, 1, dtype=BF16, device="cuda").t()
+    return [a, b, c]
+
+
+@pytest.mark.parametrize("which", range(3))
+@pytest.mark.parametrize("fmt", FMTS)
+def test_one_row_views(fg8, fmt, which):
+    """norm -> experts -> norm on one decoded token out of a larger tensor, as for the token alone."""
+    H, I, E, k = 512, 256, 4, 2
+    b = Layer(fg8, 1, k, E, H, I, fmt, seed=3)
+    x = _one_rows(H)[which]
+    x.copy_(b.x)
+    r = _one_rows(H)[which]
+    r.copy_(W.normal((1, H), 1.0, seed=9))
+    w = (1 + W.normal((H,), 0.3, seed=H).float()).to(BF16).cuda()
+
+    def chain(x, r):
+        q, s, ro, y = fg8.rmsnorm_quant(x, w, 1e-6, r, fmt, return_y=True)
+        o = b.run(fg8, x=q, x_scale=s)
+        o2 = b.run(fg8, x=x)
+        q2, s2, ro2, _ = fg8.rmsnorm_quant(o, w, 1e-6, ro, fmt)
+        a, c, v = fg8.silu_mul_quant(x, r, fmt, return_y=True)
+        return q, s, ro, y, o, o2, q2, s2, ro2, a, c, v
+    got, want = chain(x, r), chain(x.clone(memory_format=torch.contiguous_format).reshape(-1).reshape(1, H),
+                                   r.reshape(-1).clone().reshape(1, H))
+    for g, e in zip(got, want):
+        assert g.stride() == (g.shape[1], 1) and _same(g, e)
+
+
+@pytest.mark.parametrize("which", range(3))
+def test_one_row_outputs_and_linears(fg8, which):
+    H, I, E, k = 512, 256, 4, 2
+    b = Layer(fg8, 1, k, E, H, I, "float", seed=3)
+    x, out, ro = (_one_rows(H)[which] for _ in range(3))
+    x.copy_(b.x)
+    w = torch.ones(H, dtype=BF16, device="cuda")
+    assert torch.equal(b.run(fg8, out=out), b.run(fg8)) and torch.equal(out, b.run(fg8))
+    wq, ws = fg8.quantize_weight(W.normal((H, H), 0.05, seed=2).cuda(), "float")
+    y, _ = fg8.rmsnorm_linear(x, w, wq, ws, None, 1e-6, x, residual_out=ro, out=out)
+    want, want_r = fg8.rmsnorm_linear(b.x, w, wq, ws, None, 1e-6, b.x)
+    assert torch.equal(y, want) and torch.equal(ro, want_r)
+    fg8.silu_mul_linear(x, x, wq, ws, out=out)
+    assert torch.equal(out, fg8.silu_mul_linear(b.x, b.x, wq, ws))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_route_of_one_row_view(fg8, dtype):
+    l = torch.randn(64, 1, device="cuda").to(dtype).t()
+    a, b = fg8.moe_route(l, 6), fg8.moe_route(l.reshape(-1).clone().reshape(1, 64), 6)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 # -------------------------------------- silu(gate) * up, its streaming form --
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("M,K,block", [(30001, 480, 128), (3300, 4112, 64), (1700, 8208, 32), (28500, 16, 128)])
