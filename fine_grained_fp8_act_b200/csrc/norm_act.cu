@@ -28,6 +28,8 @@ namespace {
 
 using namespace qm;
 
+constexpr float kInf = __builtin_huge_valf();
+
 __device__ __forceinline__ void unpack8(const uint4& v, float2 (&f)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -113,15 +115,33 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// 1 / sqrt(mean + eps): the hardware's approximation (2^-22.9) and one Newton
-// step, y + y/2 (1 - m y y), good to an ulp or so.  m = inf gives NaN in the
-// step, so the approximation's 0 is kept there, and the rows whose squares
-// overflow float32 come out as zeros.
-__device__ __forceinline__ float row_rstd(const NormActArgs& a, float ss) {
-  const float m = fmaf(ss, a.inv_k, a.eps);
+__device__ __forceinline__ float row_mean(const NormActArgs& a, float ss) { return fmaf(ss, a.inv_k, a.eps); }
+
+// 1 / sqrt(m) of a finite m: the hardware's approximation (2^-22.9) and one
+// Newton step, y + y/2 (1 - m y y), good to an ulp or so.
+__device__ __forceinline__ float rstd_of(float m) {
   const float y = rsqrtf(m);
-  const float r = fmaf(0.5f * y, fmaf(-m * y, y, 1.0f), y);
-  return m < __int_as_float(0x7f800000) ? r : y;
+  return fmaf(0.5f * y, fmaf(-m * y, y, 1.0f), y);
+}
+
+// Rows of finite z whose m does not fit float32 (|z| from some 2^64 / sqrt(K)
+// on, or a large eps) take the squares of z 2^-80: at most 2^96, K of them
+// 2^126, while what underflows (|z| < 2^6) is nothing beside 2^128 / K.  Above
+// an rms of 2^126 the result is subnormal: 4 U off in place of a rounding's U.
+// (An infinite z: 0, so that finite elements become zeros and it NaN.)
+// Up to 3% slower than without, where there is no residual: 16384 x 12288 134
+// us against 131, one token of 2048 1.63 against 1.57.
+constexpr float kDown = 8.27180612553027674871e-25f;  // 2^-80
+__device__ __forceinline__ float rstd_of_down(const NormActArgs& a, float ss_down) {
+  const float m = fmaf(ss_down, a.inv_k, a.eps * kDown * kDown);
+  return m < kInf ? rstd_of(m) * kDown : 0.0f;
+}
+
+__device__ __forceinline__ float square_sum_down(const float2 (&z)[4], float ss) {
+  float2 d[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[i] = __fmul2_rn(z[i], make_float2(kDown, kDown));
+  return square_sum(d, ss);
 }
 
 // z of a lane's 8 channels, once the row's 1 / rms is known: the new
@@ -144,7 +164,7 @@ __device__ __forceinline__ void finish_norm(const NormActArgs& a, float2 (&z)[4]
 // flight at once; rows longer than 8 THREADS CH are read twice.
 template <int FMT, int THREADS, int CH>
 __global__ void __launch_bounds__(THREADS) rmsnorm_row_kernel(const NormActArgs a) {
-  __shared__ float red[THREADS / 32];
+  __shared__ float red[2][THREADS / 32];
   grid_wait_prerequisites();
   grid_launch_dependents();
   const int t = threadIdx.x;
@@ -182,13 +202,28 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_row_kernel(const NormActArgs 
     load(i, e);
     ss = square_sum(e, ss);
   }
-  ss = warp_sum(ss);
-  if (THREADS > 32) {
-    if ((t & 31) == 0) red[t >> 5] = ss;
-    __syncthreads();
-    ss = warp_sum((t & 31) < THREADS / 32 ? red[t & 31] : 0.0f);
+  auto row_sum = [&](float v, int set) {
+    v = warp_sum(v);
+    if (THREADS > 32) {
+      if ((t & 31) == 0) red[set][t >> 5] = v;
+      __syncthreads();
+      v = warp_sum((t & 31) < THREADS / 32 ? red[set][t & 31] : 0.0f);
+    }
+    return v;
+  };
+  const float mean = row_mean(a, row_sum(ss, 0));
+  float rstd = rstd_of(mean);
+  if (mean == kInf) {  // the same in every thread
+    ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) ss = square_sum_down(z[i], ss);
+    for (int i = CH; i < steps; ++i) {
+      float2 e[4];
+      load(i, e);
+      ss = square_sum_down(e, ss);
+    }
+    rstd = rstd_of_down(a, row_sum(ss, 1));
   }
-  const float rstd = row_rstd(a, ss);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int k = 8 * (t + i * THREADS);
@@ -339,15 +374,30 @@ __global__ void __launch_bounds__(rms_warps(S, OPS, NBUF) * 32, 1) rmsnorm_strea
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = __ffma2_rn(z[s][j], z[s][j], ss);
     }
-    float sum = warp_sum(ss.x + ss.y);
-    if (W > 1) {
-      // two sets in turn: a warp ahead by one token writes the other one
-      if (lane == 0) red[flip][warp] = sum;
-      named_barrier_sync(team, W * 32);  // at most 16 teams, 16 barriers: the CTA's own (0) is not used here
-      sum = warp_sum(lane < W ? red[flip][team * W + lane] : 0.0f);
-      flip ^= 1;
+    auto team_sum = [&](float v) {
+      v = warp_sum(v);
+      if (W > 1) {
+        // two sets in turn: a warp ahead by one sum writes the other one
+        if (lane == 0) red[flip][warp] = v;
+        named_barrier_sync(team, W * 32);  // at most 16 teams, 16 barriers: the CTA's own (0) is not used here
+        v = warp_sum(lane < W ? red[flip][team * W + lane] : 0.0f);
+        flip ^= 1;
+      }
+      return v;
+    };
+    const float mean = row_mean(a, team_sum(ss.x + ss.y));
+    float rstd = rstd_of(mean);
+    if (mean == kInf) {  // the same in the whole team
+      ss = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 d = __fmul2_rn(z[s][j], make_float2(kDown, kDown));
+          ss = __ffma2_rn(d, d, ss);
+        }
+      rstd = rstd_of_down(a, team_sum(ss.x + ss.y));
     }
-    const float rstd = row_rstd(a, sum);
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       const bool real = k0 + s * 512 < a.K;

@@ -380,8 +380,9 @@ FG8_API fg8_status fg8_scale_to_ue8m0(const void* scale_f32, int64_t n, void* sc
 /* RMS norm of x (with a residual added first), quantized as an activation in
  * one pass: the layer in front of a block's first FP8 linear.
  *   z = x + residual;  v = z * (1 / sqrt(mean(z^2) + eps)) * weight
- * in float32, then scales and codes of v exactly as fg8_quantize_act_block
- * makes them of its input (v itself is not rounded to bf16 first).
+ * in float32 (rows of finite z whose squares pass float32 included), then
+ * scales and codes of v exactly as fg8_quantize_act_block makes them of its
+ * input (v itself is not rounded to bf16 first).
  *   x_bf16        [M, K] bf16, row stride ld_x
  *   residual_bf16 [M, K] bf16, row stride ld_residual, or NULL (z = x)
  *   weight_bf16   [K] bf16

@@ -68,6 +68,44 @@ def test_rmsnorm_value_past_float32(fg8, fmt, M, K, block):
     _check_overflowed(fg8, fmt, got, clean, got[3], m, block)
 
 
+# ----------------------------------- rows whose squares are past float32 ----
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("M,K", [(6, 256), (6, 16400), (6, 30000), (10000, 256), (1300, 4112), (2500, 4096),
+                                 (700, 16400)])
+def test_rmsnorm_squares_past_float32(fg8, fmt, residual, M, K):
+    """Finite rows whose sum of squares overflows float32 are normalized like all others: the mean square is then
+    taken of z 2^-80.  1 / rms may be subnormal there, 4 U off instead of its rounding's 1 U."""
+    x = W.normal((M, K), 1.0, seed=M + K).float().cuda()
+    top = 3.3e38 if not residual else 1.6e38
+    m = torch.arange(M, device="cuda")
+    x[m % 5 == 1] *= 2.0 ** 64                                     # squares alone reach 2^128
+    x[m % 5 == 2] = x[m % 5 == 2].sign() * top                     # nothing larger exists
+    x[m % 5 == 3] = 0
+    x[m % 5 == 3, 7] = 2.0 ** 100                                  # one element
+    x[m % 5 == 4] *= 2.0 ** 61                                     # the sum, not its terms
+    x = x.to(BF16)
+    r = x.clone() if residual else None
+    w = (1 + W.normal((K,), 0.3, seed=K).float()).to(BF16).cuda()
+    xq, xs, ro, y = fg8.rmsnorm_quant(x, w, 1e-6, r, fmt, return_y=True)
+    z, v, err = P.rmsnorm(x, w, float(np.float32(1e-6)), r)
+    err = err + v.abs() * 4 * P.U
+    P.check_quantized(xq, xs, v, err, fmt, 128, "rmsnorm")
+    assert bool(((y.to(F64) - v).abs() <= v.abs() * 2.0 ** -8 + err).all())
+    if residual:
+        assert torch.equal(ro, (x.float() + r.float()).to(BF16))
+
+
+def test_rmsnorm_large_eps(fg8):
+    """mean square + eps past float32 although both are finite."""
+    x = torch.full((4, 256), 1.5e19, dtype=BF16, device="cuda")
+    w = torch.ones(256, dtype=BF16, device="cuda")
+    eps = 2.5e38
+    xq, xs, _, _ = fg8.rmsnorm_quant(x, w, eps, None, "float")
+    _, v, err = P.rmsnorm(x, w, float(np.float32(eps)), None)
+    P.check_quantized(xq, xs, v, err + v.abs() * 4 * P.U, "float", 128)
+
+
 # ----------------------------------------------------------- one-row views --
 def _one_rows(K):
     """One row at strides that are not its length: hidden[:, -1] of a batch of one, a buffer whose width is no
