@@ -118,8 +118,8 @@ def fg8_set_wait_limit_ns(ns: int) -> None:
     lib().fg8_set_wait_limit_ns(int(ns))
 
 
-def fg8_set_test_stall(on: bool) -> None:
-    lib().fg8_set_test_stall(1 if on else 0)
+def fg8_set_test_stall(on: int) -> None:
+    lib().fg8_set_test_stall(int(on))
 
 
 def fg8_quantize_weight(w_bf16, N, K, ld_w, wq_e4m3, w_scale_inv, fmt, stream):

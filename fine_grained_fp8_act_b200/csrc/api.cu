@@ -25,6 +25,7 @@ constexpr size_t kAlign = 256;
 
 std::atomic<uint64_t> g_wait_limit_ns{2000000000ull};
 std::atomic<int> g_test_stall{0};
+std::atomic<int> g_test_late{0};
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
@@ -310,7 +311,10 @@ const char* fg8_status_string(fg8_status st) {
 
 void fg8_set_wait_limit_ns(uint64_t ns) { g_wait_limit_ns.store(ns); }
 
-void fg8_set_test_stall(int on) { g_test_stall.store(on != 0 ? 1 : 0); }
+void fg8_set_test_stall(int on) {
+  g_test_stall.store(on != 0 && on != 2 ? 1 : 0);
+  g_test_late.store(on == 2 ? 1 : 0);
+}
 
 fg8_status fg8_quantize_weight(const void* w_bf16, int64_t N, int64_t K, int64_t ld_w, void* wq_e4m3,
                                void* w_scale_inv, fg8_scale_fmt fmt, void* stream) {
@@ -1281,6 +1285,7 @@ fg8_status fg8_moe_mlp(const void* x, const void* x_scale, int64_t T, int64_t H,
   a.ws = static_cast<uint8_t*>(workspace);
   a.wait_limit_ns = g_wait_limit_ns.load();
   a.test_stall = g_test_stall.load();
+  a.test_late = g_test_late.load();
   return cuda_status(launch_moe_mlp(a, fmt, dev.sms, static_cast<cudaStream_t>(stream)));
 }
 

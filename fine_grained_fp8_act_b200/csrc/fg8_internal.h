@@ -110,6 +110,7 @@ struct MoeArgs {
   uint8_t* ws;         // workspace (moe_ws_layout)
   uint64_t wait_limit_ns;
   int test_stall;
+  int test_late;       // test hook: the first kernel's CTA 0 idles for three wait limits
 };
 size_t moe_workspace_need(int T, int k, int E, int H, int I, int fmt);
 cudaError_t launch_moe_mlp(const MoeArgs& a, int fmt, int num_sms, cudaStream_t s);

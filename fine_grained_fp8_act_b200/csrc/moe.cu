@@ -40,8 +40,11 @@
 //               (UP); the pairs' products, and by the last CTA of a row tile
 //               the weighted sums over the slots (DOWN).
 //
-// DOWN is launched to overlap UP's end: its first weight tiles are on their
-// way while UP's last units finish; only the warps that read h wait for it.
+// DOWN is launched to overlap UP's end: its first weight tiles, one ring of
+// them, are on their way while UP's last units finish.  Then every role waits
+// for UP before its first bounded wait and before it touches the workspace: how
+// long UP still takes must not count against DOWN's limit, and the partial
+// sums and counters are UP's until then.
 // (Having UP's producers bring DOWN's first 5, 8 or 12 K-blocks per CTA into
 // L2 at their end changed nothing: 70.4 to 71.0 us against 70.4 for one token
 // over 8 experts of 7168 x 2048.)
@@ -127,7 +130,7 @@ struct MoeParams {
   uint32_t* status;
   uint32_t* counters;
   uint64_t wait_limit_ns;
-  int test_stall;
+  int test_stall, test_late;
 };
 
 enum Phase : int { UP = 0, DOWN = 1 };
@@ -408,6 +411,7 @@ __device__ __forceinline__ void moe_producer(const CUtensorMap* tmW, const MoePa
     const bool second = has_second<C>(p, walk.tile);
     for (int kb = walk.k0; kb < walk.k1; ++kb, ++it) {
       const int slot = static_cast<int>(it % C::STAGES);
+      if (C::PHASE == DOWN && it == C::STAGES) grid_wait_prerequisites();  // the ring is full
       if (!mbar_wait(b.empty + slot, static_cast<uint32_t>((it / C::STAGES) & 1) ^ 1u, p.wait_limit_ns, b.abort_flag)) {
         moe_raise(p, b);
         ok = false;
@@ -428,6 +432,7 @@ template <class C>
 __device__ __forceinline__ void moe_mma(const MoeParams& p, const Routing& r, uint8_t* smem, uint32_t tmem,
                                         const Bars& b, Walk walk) {
   bool ok = true;
+  if (C::PHASE == DOWN) grid_wait_prerequisites();
   // test hook: a barrier nothing arrives on, so the bounded wait runs out
   if (p.test_stall && !mbar_wait(b.stall, 0, p.wait_limit_ns, b.abort_flag)) {
     moe_raise(p, b);
@@ -760,6 +765,7 @@ __device__ __forceinline__ void moe_epilogue(const MoeParams& p, const Routing& 
   // the box's weight scale: the second box of UP may lie in two scale blocks
   const int at = kChunk + (half == 0 ? 0 : (C::PHASE == UP && row >= 128 - p.I % 128) ? 2 : 1);
   float* stage = reinterpret_cast<float*>(smem + C::kOffStage);
+  if (C::PHASE == DOWN) grid_wait_prerequisites();
   uint32_t it = 0;
   bool ok = true;
   while (walk.next(r)) {
@@ -885,6 +891,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   // UP, which waited itself; only h is new.
   if (C::PHASE == UP) grid_wait_prerequisites();
   grid_launch_dependents();
+  if (C::PHASE == UP && p.test_late && blockIdx.x == 0 && threadIdx.x == 0)  // test hook
+    for (const uint64_t t0 = global_timer_ns(); global_timer_ns() - t0 < 3 * p.wait_limit_ns;) __nanosleep(100000);
   count_pairs(p, r);
   __syncthreads();
   if (warp == C::kFillWarp0) {
@@ -1035,6 +1043,7 @@ cudaError_t launch_moe_mlp(const MoeArgs& a, int fmt, int num_sms, cudaStream_t 
   p.counters = reinterpret_cast<uint32_t*>(a.ws + kHeaderCounterOffset);
   p.wait_limit_ns = a.wait_limit_ns;
   p.test_stall = a.test_stall;
+  p.test_late = a.test_late;
   MoeParams up = p, down = p;
   up.w_scale = a.s13;
   up.K = a.H;

@@ -501,7 +501,9 @@ FG8_API void fg8_set_wait_limit_ns(uint64_t ns);
  * mbarrier that nothing completes, so its bounded wait runs out after the
  * wait limit; the kernel then records FG8_ERR_TIMEOUT in the status word,
  * drains its own copies and tensor-core ops, frees TMEM and returns.  No
- * fault and no unbounded wait are involved.  Not for production use. */
+ * fault and no unbounded wait are involved.  on == 2: nothing waits in vain,
+ * but one CTA of fg8_moe_mlp's first kernel idles for three wait limits, which
+ * its second kernel has to sit out.  Not for production use. */
 FG8_API void fg8_set_test_stall(int on);
 
 /* Static description of a status code. */
