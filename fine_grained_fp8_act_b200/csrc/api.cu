@@ -312,8 +312,8 @@ const char* fg8_status_string(fg8_status st) {
 void fg8_set_wait_limit_ns(uint64_t ns) { g_wait_limit_ns.store(ns); }
 
 void fg8_set_test_stall(int on) {
-  g_test_stall.store(on != 0 && on != 2 ? 1 : 0);
-  g_test_late.store(on == 2 ? 1 : 0);
+  g_test_stall.store(on == 2 ? 0 : on);
+  g_test_late.store(on == 2 || on == 3 ? on - 1 : 0);
 }
 
 fg8_status fg8_quantize_weight(const void* w_bf16, int64_t N, int64_t K, int64_t ld_w, void* wq_e4m3,

@@ -109,8 +109,8 @@ struct MoeArgs {
   int64_t ld_y;
   uint8_t* ws;         // workspace (moe_ws_layout)
   uint64_t wait_limit_ns;
-  int test_stall;
-  int test_late;       // test hook: the first kernel's CTA 0 idles for three wait limits
+  int test_stall;      // 3: in the first kernel alone
+  int test_late;       // test hook: CTA 0 of the first (1) or second (2) kernel idles for three wait limits
 };
 size_t moe_workspace_need(int T, int k, int E, int H, int I, int fmt);
 cudaError_t launch_moe_mlp(const MoeArgs& a, int fmt, int num_sms, cudaStream_t s);

@@ -206,6 +206,9 @@ __device__ __forceinline__ void clear_counts(const MoeParams& p, const Routing& 
   }
 }
 
+// UP reports an expert out of range (once: DOWN has the same ids), and never
+// over a timeout, after which y is unspecified as a whole.
+template <int PHASE>
 __device__ __forceinline__ void count_pairs(const MoeParams& p, const Routing& r) {
   const int P = p.T * p.k;
   for (int i = threadIdx.x; i < P; i += blockDim.x) {
@@ -214,7 +217,7 @@ __device__ __forceinline__ void count_pairs(const MoeParams& p, const Routing& r
     if (p.weights != nullptr) prefetch_l1(p.weights + i);  // for the sums at the end
     r.ids[i] = on ? static_cast<uint16_t>(id) : static_cast<uint16_t>(0xFFFFu);
     if (on) atomicAdd(r.count + id, 1u);
-    else if (id >= 0 && blockIdx.x == 0) atomicExch(p.status, kInvalidArgStatus);
+    else if (PHASE == UP && id >= 0 && blockIdx.x == 0) atomicCAS(p.status, 0u, kInvalidArgStatus);
   }
 }
 
@@ -891,9 +894,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   // UP, which waited itself; only h is new.
   if (C::PHASE == UP) grid_wait_prerequisites();
   grid_launch_dependents();
-  if (C::PHASE == UP && p.test_late && blockIdx.x == 0 && threadIdx.x == 0)  // test hook
+  if (p.test_late == C::PHASE + 1 && blockIdx.x == 0)  // test hook
     for (const uint64_t t0 = global_timer_ns(); global_timer_ns() - t0 < 3 * p.wait_limit_ns;) __nanosleep(100000);
-  count_pairs(p, r);
+  count_pairs<C::PHASE>(p, r);
   __syncthreads();
   if (warp == C::kFillWarp0) {
     const int jobs = place_experts(p, r);
@@ -1056,6 +1059,7 @@ cudaError_t launch_moe_mlp(const MoeArgs& a, int fmt, int num_sms, cudaStream_t 
   down.Nb = Hb;
   down.tiles = (a.H + kRowTile - 1) / kRowTile;
   up.weights = nullptr;  // only DOWN sums
+  if (a.test_stall == 3) down.test_stall = 0;
   return fmt == 0 ? launch_fmt<0>(a, up, down, num_sms, s) : launch_fmt<1>(a, up, down, num_sms, s);
 }
 

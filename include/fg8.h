@@ -489,7 +489,7 @@ FG8_API fg8_status fg8_moe_mlp(const void* x, const void* x_scale, int64_t T, in
  * FG8_OK; FG8_ERR_TIMEOUT if one of its device-side waits gave up (the
  * kernel then returned early; y is unspecified); FG8_ERR_INVALID_ARG if
  * fg8_grouped_linear or fg8_moe_mlp met an expert index >= E (those blocks
- * or slots were skipped). */
+ * or slots were skipped; fg8_moe_mlp keeps a timeout where both happened). */
 FG8_API fg8_status fg8_check_device_status(void* workspace, void* stream);
 
 /* Upper bound, in nanoseconds, on any single device-side wait of the GEMM
@@ -503,7 +503,9 @@ FG8_API void fg8_set_wait_limit_ns(uint64_t ns);
  * drains its own copies and tensor-core ops, frees TMEM and returns.  No
  * fault and no unbounded wait are involved.  on == 2: nothing waits in vain,
  * but one CTA of fg8_moe_mlp's first kernel idles for three wait limits, which
- * its second kernel has to sit out.  Not for production use. */
+ * its second kernel has to sit out; on == 3: the first kernel's MMA threads
+ * wait in vain, the second one's do not, and one of its CTAs idles until after
+ * the first one's timeouts.  Not for production use. */
 FG8_API void fg8_set_test_stall(int on);
 
 /* Static description of a status code. */

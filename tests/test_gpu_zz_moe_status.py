@@ -44,3 +44,28 @@ def test_second_kernel_sits_out_a_slow_first(fg8, T, k, E, H, I, fmt):
     assert torch.equal(y, want)
     assert bool((ws[:1024] == 0).all())                          # status word and counters at rest
     assert torch.equal(a.run(fg8, workspace=ws), want)
+
+
+@pytest.mark.parametrize("T,k,E,H,I,fmt", [(5, 2, 4, 512, 256, "float"), (40, 4, 8, 2048, 640, "ue8m0")])
+def test_timeout_outlives_a_bad_expert(fg8, T, k, E, H, I, fmt):
+    """The first kernel times out on routing that also names an expert out of range: y is unspecified then, and the
+    status says so, rather than that some slots were skipped."""
+    a = Layer(fg8, T, k, E, H, I, fmt, seed=6)
+    ws = _workspace(fg8, T, k, E, H, I, fmt)
+    s = torch.cuda.current_stream().cuda_stream
+    good = a.ids.clone()
+    a.ids[1, 0] = E
+    try:
+        fg8.fg8_set_wait_limit_ns(40_000_000)
+        fg8.fg8_set_test_stall(3)
+        a.run(fg8, workspace=ws)
+        torch.cuda.synchronize()
+        assert fg8.fg8_check_device_status(ws.data_ptr(), s) == fg8.FG8_ERR_TIMEOUT
+    finally:
+        fg8.fg8_set_test_stall(0)
+        fg8.fg8_set_wait_limit_ns(2_000_000_000)
+    a.run(fg8, workspace=ws)
+    assert fg8.fg8_check_device_status(ws.data_ptr(), s) == fg8.FG8_ERR_INVALID_ARG
+    a.ids.copy_(good)
+    a.check(a.run(fg8, workspace=ws))
+    assert fg8.fg8_check_device_status(ws.data_ptr(), s) == fg8.FG8_OK
