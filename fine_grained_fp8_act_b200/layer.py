@@ -173,6 +173,19 @@ def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor]) -> torch.
     return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
+_HEADER = 1024  # bytes of status word and counters
+
+
+def _workspace_behind_header(nbytes: int, device, workspace: Optional[torch.Tensor]) -> torch.Tensor:
+    """_workspace for the operators around the linears, a new one with its header alone zeroed: what lies behind it is
+    written before it is read, and one token's expert layer has over 10 MB of it."""
+    if workspace is not None:
+        return _workspace(nbytes, device, workspace)
+    ws = torch.empty(max(nbytes, _HEADER), dtype=torch.uint8, device=device)
+    ws[:_HEADER].zero_()
+    return ws
+
+
 def linear(x: torch.Tensor, wq: torch.Tensor, w_scale_inv: torch.Tensor, bias: Optional[torch.Tensor] = None,
            scale_fmt="float", out: Optional[torch.Tensor] = None,
            workspace: Optional[torch.Tensor] = None, block: int = 128) -> torch.Tensor:
@@ -353,7 +366,7 @@ def scale_to_ue8m0(scale: torch.Tensor) -> Tuple[torch.Tensor, int]:
 # an operand's shape and stride are read once, outputs come from the cheapest
 # allocating call (empty_like, then new_empty with sizes spelled out).
 def _like(x: torch.Tensor, dtype=torch.bfloat16) -> torch.Tensor:
-    """A new row-major tensor of x's shape.  (Without the format one row would hand on its own stride, contiguous or not.)"""
+    """A new row-major tensor of x's shape.  (Without the format a single row would hand on whatever stride it has.)"""
     return torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
 
 
@@ -436,7 +449,7 @@ def _linear_operands(x: torch.Tensor, wq, w_scale_inv, bias, fmt: int, out, work
     bp = _check_bias(bias, (N,), x.device)
     y = _output(out, M, N, x.device)
     _check_cuda(x, "x")
-    return N, bp, y, _workspace(C.fg8_linear_workspace_bytes(M, N, K, fmt), x.device, workspace)
+    return N, bp, y, _workspace_behind_header(C.fg8_linear_workspace_bytes(M, N, K, fmt), x.device, workspace)
 
 
 def rmsnorm_linear(x: torch.Tensor, weight: torch.Tensor, wq: torch.Tensor, w_scale_inv: torch.Tensor,
@@ -543,7 +556,7 @@ def moe_mlp(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: torc
     _check_tensor(w2_scale_inv, "w2_scale_inv", (E, Hb, _cdiv(I, 128)), scales, device)
     y = _like(x) if out is None else _output(out, T, H, device)
     _check_cuda(x, "x")
-    ws = _workspace(_moe_workspace_bytes(T, k, E, H, I, fmt), device, workspace)
+    ws = _workspace_behind_header(_moe_workspace_bytes(T, k, E, H, I, fmt), device, workspace)
     with _on(device):
         C.fg8_moe_mlp(x.data_ptr(), 0 if x_scale is None else x_scale.data_ptr(), T, H, ld, ids.data_ptr(),
                       weights.data_ptr(), k, E, I, w13.data_ptr(), w13_scale_inv.data_ptr(), w2.data_ptr(),

@@ -217,3 +217,43 @@ def test_silu_mul_extreme_gates_streamed(fg8, fmt):
     v, err = P.silu_mul(g, u)
     P.check_quantized(xq, xs, v, err + 2.0 ** -149, fmt, 128)
     assert bool(((y.to(F64) - v).abs() <= v.abs() * 2.0 ** -8 + err + 2.0 ** -134).all())
+
+
+# --------------------------------------------- workspaces made for the call --
+def _leave_noise(n):
+    """n bytes of 0xA5 left behind in the caching allocator, for the next allocation of this size."""
+    for _ in range(2):
+        t = torch.full((n,), 0xA5, dtype=U8, device="cuda")
+        torch.cuda.synchronize()
+        del t
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,k,E,H,I", [(1, 2, 4, 256, 128), (40, 4, 8, 2064, 1424), (100, 2, 4, 528, 272)])
+def test_moe_mlp_on_used_memory(fg8, fmt, T, k, E, H, I):
+    """Without a workspace argument the layer runs on memory that held something else."""
+    a = Layer(fg8, T, k, E, H, I, fmt, seed=T)
+    a.ids[T // 2] = -1
+    a.w[T // 2] = float("nan")
+    n = fg8.fg8_moe_mlp_workspace_bytes(T, k, E, H, I, fg8.scale_fmt_code(fmt))
+    want = a.run(fg8, workspace=torch.zeros(n, dtype=U8, device="cuda"))
+    for _ in range(3):
+        _leave_noise(n)
+        assert torch.equal(a.run(fg8), want)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,K,N", [(5, 400, 264), (130, 1040, 256), (256, 8192, 1024)])
+def test_linears_on_used_memory(fg8, fmt, M, K, N):
+    x, r = W.x_outliers(M, K, seed=M).cuda(), W.normal((M, K), 1.0, seed=K).cuda()
+    nw = torch.ones(K, dtype=BF16, device="cuda")
+    wq, ws = fg8.quantize_weight(W.normal((N, K), 0.05, seed=N).cuda(), fmt)
+    n = fg8.fg8_linear_workspace_bytes(M, N, K, fg8.scale_fmt_code(fmt))
+    wsp = torch.zeros(n, dtype=U8, device="cuda")
+    want = (fg8.rmsnorm_linear(x, nw, wq, ws, None, 1e-6, r, fmt, workspace=wsp)[0],
+            fg8.silu_mul_linear(x, r, wq, ws, None, fmt, workspace=wsp))
+    for _ in range(3):
+        _leave_noise(n)
+        assert torch.equal(fg8.rmsnorm_linear(x, nw, wq, ws, None, 1e-6, r, fmt)[0], want[0])
+        _leave_noise(n)
+        assert torch.equal(fg8.silu_mul_linear(x, r, wq, ws, None, fmt), want[1])
