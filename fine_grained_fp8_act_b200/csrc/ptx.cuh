@@ -306,8 +306,9 @@ __device__ __forceinline__ void tmem_reg_fence(uint32_t* r) {
   tmem_reg_fence16(r + 16);
 }
 
-// Barrier `id` (1..15) over the first `count` threads that reach it (a
-// multiple of 32): synchronizes a subset of the CTA's warps.
+// Barrier `id` over the first `count` threads that reach it (a multiple of
+// 32): synchronizes a subset of the CTA's warps.  1..15, or 0 too in a kernel
+// without __syncthreads(), whose barrier that is.
 __device__ __forceinline__ void named_barrier_sync(uint32_t id, uint32_t count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }

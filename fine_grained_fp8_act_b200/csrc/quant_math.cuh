@@ -85,8 +85,12 @@ __device__ __forceinline__ float rcp_approx(float x) {  // 1 / x within one ulp,
 // silu(g) * u for two values, in float32: g / (1 + e) * u with e = exp(-g) =
 // 2^t.  t = -g log2(e) is carried as a float and its remainder, t = hn - 2 r,
 // and 2^t = 2^hn (1 - 2 r ln 2): the remainder would cost |g| 2^-25 of e
-// otherwise.  About 10 2^-24 relative in all: e 4 (2^-22) and 1/2 for its
-// factor, then the sum, the reciprocal (an ulp), two products.
+// otherwise.  At most some 10 2^-24 relative in all: e 4 (2^-22) and 1/2 for
+// its factor, then the sum, the reciprocal (an ulp), two products.  On 16.8M
+// normal gates the mean is 0.82 2^-24 and the largest 4.3, where expf and a
+// rounded division (torch's float32 form) have 0.71 and 3.5; of 127M codes made
+// of either, 189 and 191 differ from the 64-bit ones.  So all kernels take
+// the cheap form, and a row's codes do not depend on how many rows there are.
 // No finite gate needs a clamp.  Below -88 e overflows to inf, times a
 // factor of either sign, and 1 / d is a zero; from -87.336 on, where 1 / d is
 // no normal float32, it is 0 already (all of silu's 88 2^-126 there).  Above
@@ -121,7 +125,8 @@ __device__ __forceinline__ float group_scale_fast(float amax) {
 }
 
 // Codes of values v that float32 arithmetic made (not of given bf16 values),
-// which come NEGATED, n = -v.  The quotient takes one FMA correction of
+// which come NEGATED, n = -v.  (Behind the RMS norm 766 and 780 of 105M codes
+// differ from the 64-bit ones in float32 torch and here.)  The quotient takes one FMA correction of
 // q0 = v y, y the approximate 1/s: q1 = q0 - (q0 s - v) y.  q0 is within 3 ulp
 // of v / s, so the correction is right to 2^-21 ulp before q1's rounding: q1
 // is v / s where that is a float32 (ties between two codes are kept) and next

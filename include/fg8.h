@@ -407,7 +407,8 @@ FG8_API fg8_status fg8_rmsnorm_quant(const void* x_bf16, int64_t M, int64_t K, i
 /* silu(gate) * up, quantized as an activation in one pass: what stands
  * between a gate/up projection and the down projection.
  *   v = gate / (1 + exp(-gate)) * up
- * in float32, then scales and codes of v as fg8_quantize_act_block's.
+ * in float32, then scales and codes of v as fg8_quantize_act_block's.  (Where
+ * 1 / (1 + exp(-gate)) is no normal float32, gate < -87.336, it is taken as 0.)
  *   gate_bf16, up_bf16 [M, K] bf16, row strides ld_gate, ld_up (the two
  *                 halves of one [M, 2K] output have ld = 2K and up = gate + K)
  *   xq_e4m3, x_scale, block, y_bf16 as fg8_rmsnorm_quant.  No output overlaps
@@ -465,7 +466,7 @@ FG8_API fg8_status fg8_moe_route(const void* logits, int logits_bf16, int64_t T,
  *            another rank, padding); an id >= E is skipped too and leaves
  *            FG8_ERR_INVALID_ARG in the status word.  The same expert may
  *            stand in several slots of a token: each counts.
- *   weights  [T, k] float32
+ *   weights  [T, k] float32; those of skipped slots are not used
  *   w13_e4m3 [E, 2I, H] e4m3fn: the I gate rows, then the I up rows;
  *            w13_scale_inv [E, ceil(2I/128), ceil(H/128)]
  *   w2_e4m3  [E, H, I] e4m3fn; w2_scale_inv [E, ceil(H/128), ceil(I/128)]
@@ -476,7 +477,8 @@ FG8_API fg8_status fg8_moe_route(const void* logits, int logits_bf16, int64_t T,
  * The reached experts' weights stream once for up to 32 slots per expert and
  * again, out of L2, for every further 32: far above that fg8_grouped_linear
  * is faster.  T <= 256, k <= 32, T * k <= 4096, E <= 1024, H <= 16384, I <= 2^20,
- * H % 16 == 0, I % 16 == 0, E * 2I + 256 and E * H + 256 <= 2^31 - 1.  T == 0 is a no-op. */
+ * H % 16 == 0, I % 16 == 0; x, y, the weights and both w*_scale_inv 16-byte
+ * aligned (mind slices of the scales); E * 2I + 256 and E * H + 256 <= 2^31 - 1.  T == 0 is a no-op. */
 FG8_API size_t fg8_moe_mlp_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, fg8_scale_fmt fmt);
 FG8_API fg8_status fg8_moe_mlp(const void* x, const void* x_scale, int64_t T, int64_t H, int64_t ld_x,
                                const int32_t* ids, const float* weights, int64_t k, int64_t E, int64_t I,
