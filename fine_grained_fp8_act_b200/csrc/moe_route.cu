@@ -11,7 +11,8 @@
 // such keys (many equal logits, k near 32) is chosen from one round at a time.
 //
 // 16384 tokens of 256 experts read 17 MB (2.6 us) and take 8.7 us, bound by
-// instructions: choosing every token by k rounds over all keys took 16 us.
+// instructions: 453 a token are 6.4 us of all issue slots, which are 78% busy
+// while warps run.  Choosing every token by k rounds over all keys took 16 us.
 //
 // exp(l - l_max) of the k chosen ones (or, without renormalization, of all)
 // is summed in float32 in a fixed order.

@@ -558,19 +558,19 @@ cudaError_t launch_rms(const NormActArgs& a, int num_sms, cudaLaunchConfig_t& cf
   // Two steps a warp: fewer shuffles and barriers a channel.  Up to eight
   // steps it makes no difference, and for 25 to 32 there would be one team of
   // 16 warps at most.  us, two steps / one, float scales, 16384 tokens with a
-  // residual and without: x 12288 216 / 248, 132 / 144; x 8192 148 / 153,
-  // 88 / 90; x 5632 105 / 109, 67 / 72; but x 6144 124 / 118, 67 / 73.
+  // residual and without: x 12288 216 / 234, 134 / 148; x 8192 146 / 157,
+  // 91 / 93; x 5632 104 / 105, 68 / 73; but x 6144 121 / 116, 69 / 75.
   const int S = n <= 8 || (n > 24 && n <= 32) ? 1 : 2, W = (n + S - 1) / S;
   const int most = S == 1 ? 32 : 24;
   if (W <= most) {
     const int teams = most / W, warps = teams * W;  // (16 teams at most where W > 1: 16 hardware barriers)
     // The rings pay from a few tokens on; below that the one-row kernel has
     // more loads in flight.  Times of row kernel / stream, without and with a
-    // residual: two steps a warp (by tokens an SM) 300 x 7168 (2) 1.40, 1.12;
-    // 450 x 7168 (3) 1.21, 0.97; 300 x 12288 (2) 1.14, 0.88; 450 x 12288 (3)
-    // 1.42, 1.08; one step (by tokens a team) 900 x 4096 (1.5) 1.10, 0.81; 2400
-    // x 4096 (4) 1.37, 0.97; 3600 x 4096 (6) 1.51, 1.33; 2400 x 2048 (2) 1.00,
-    // 0.73; and 16384 x 512 with one (3) 1.8.
+    // residual: two steps a warp (by tokens an SM) 300 x 7168 (2) 1.39, 1.12;
+    // 450 x 7168 (3) 1.20, 0.95; 300 x 12288 (2) 1.16, 0.89; 450 x 12288 (3)
+    // 1.43, 1.10; one step (by tokens a team) 900 x 4096 (1.5) 1.17, 0.84; 2400
+    // x 4096 (4) 1.39, 0.98; 3600 x 4096 (6) 1.52, 1.35; 2400 x 2048 (2) 0.99,
+    // 0.73; and 16384 x 512 with one (3) 1.6.
     const int halves = S == 2 ? (a.x2 == nullptr ? 4 : 6) : (n == 1 ? 4 : a.x2 == nullptr ? 3 : 8) * teams;
     if (2 * static_cast<int64_t>(a.M) >= static_cast<int64_t>(halves) * num_sms) {
       cfg.gridDim = dim3(static_cast<unsigned>(num_sms));
