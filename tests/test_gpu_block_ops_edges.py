@@ -243,7 +243,7 @@ def test_moe_mlp_on_used_memory(fg8, fmt, T, k, E, H, I):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("M,K,N", [(5, 400, 264), (130, 1040, 256), (256, 8192, 1024)])
+@pytest.mark.parametrize("M,K,N", [(5, 400, 264), (130, 1040, 256), (256, 8192, 1024), (3, 2064, 40000)])
 def test_linears_on_used_memory(fg8, fmt, M, K, N):
     x, r = W.x_outliers(M, K, seed=M).cuda(), W.normal((M, K), 1.0, seed=K).cuda()
     nw = torch.ones(K, dtype=BF16, device="cuda")
